@@ -23,10 +23,18 @@ from __future__ import annotations
 
 __all__ = ["prefill", "decode_step", "decode_tokens", "prefill_varlen", "kda_prefill",
            "kda_prefill_varlen", "kda_decode", "abi_version", "status_str", "query_status",
-           "GDNError"]
+           "GDNError", "scan", "scan_varlen", "scan_step", "scan_backward",
+           "scan_varlen_backward"]
+
+_RECURRENCE = ("scan", "scan_varlen", "scan_step", "scan_backward", "scan_varlen_backward")
 
 
 def __getattr__(name):
+    if name in _RECURRENCE:
+        import importlib
+        value = getattr(importlib.import_module(__name__ + ".recurrence"), name)
+        globals()[name] = value  # later uses find it without this function
+        return value
     if name in ("prefill", "decode_step", "decode_tokens", "prefill_varlen", "kda_prefill",
                 "kda_prefill_varlen", "kda_decode", "abi_version", "status_str", "query_status", "GDNError",
                 "library_path"):

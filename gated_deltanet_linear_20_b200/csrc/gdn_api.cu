@@ -13,12 +13,16 @@
 #include <cstring>
 #include <mutex>
 
+#include "gdn_host.h"
 #include "gdn_internal.h"
 
 // Built-in scratch of gdn_prefill_static_ws (no allocation anywhere).
 static __device__ __align__(256) unsigned char g_static_ws[GDN_STATIC_WORKSPACE_BYTES];
 
 namespace {
+
+using gdn::aligned;
+using gdn::overlaps;
 
 constexpr int kHeadDim = 128;
 
@@ -34,14 +38,6 @@ PFN_cuTensorMapEncodeTiled_v12000 get_encode_fn() {
       fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
   });
   return fn;
-}
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
-  if (!a || !b || na == 0 || nb == 0) return false;
-  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
-  return a0 < b0 + nb && b0 < a0 + na;
 }
 
 // Per-device facts queried once: compute capability and multiprocessor count.
@@ -365,6 +361,11 @@ bool ensure_smem_attr(const void* func, int slot, int bytes) {
   return true;
 }
 }  // namespace gdn
+
+int gdn::require_device(int* sms) {
+  const int rc = check_device();
+  return rc != GDN_OK ? rc : num_sms(sms);
+}
 
 extern "C" {
 

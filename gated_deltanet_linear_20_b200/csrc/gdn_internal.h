@@ -100,6 +100,31 @@ struct KdaArgs {
   int n_snaps = 0;                  // slots in snaps
 };
 
+// Channel recurrence over N sequences of T tokens (cu_seqlens null), or of T
+// packed tokens in all.
+struct ScanArgs {
+  const void* x;         // [tokens][C]
+  const float* g;        // [tokens][C] natural-log decays
+  const void* beta;      // [tokens][C] or null (1)
+  const float* h0;       // [N][C] or null (zeros)
+  void* h;               // [tokens][C] or null (not written)
+  float* h_T;            // [N][C]
+  float* carries;        // states before every 16th token, or null
+  const int* cu_seqlens; // [N + 1] or null
+  int N, T, C;
+  int cblocks;           // channel blocks per sequence (set by the launch)
+  int* status;           // may be null
+};
+struct ScanBackwardArgs {
+  ScanArgs f;            // inputs of the forward call and its carries
+  const void* dh;        // [tokens][C]
+  const float* dh_T;     // [N][C] or null (zeros)
+  void* dx;
+  float* dg;
+  void* dbeta;           // null without beta
+  float* dh0;            // [N][C] or null (not wanted)
+};
+
 // Sets the dynamic shared-memory limit of `func` to `bytes` once per device
 // (slot: a small per-kernel index); returns false if the attribute call failed.
 bool ensure_smem_attr(const void* func, int slot, int bytes);
@@ -124,5 +149,11 @@ int launch_segment_fix(const PrefillArgs& a, cudaStream_t stream);
 int launch_rows(const RowArgs& a, int Dk, bool vector_gate, int num_sms, cudaStream_t stream);
 int rows_per_cta(long long heads, int Dv, int num_sms);
 bool rows_head_dims_ok(int Dk, int Dv);
+
+// Channel recurrence: GDN_OK, or a negative code.  dtype is x's, beta's and h's
+// (GDN_F32 or GDN_BF16).  The step updates a.h_T in place.
+int launch_scan(const ScanArgs& a, int dtype, int sms, cudaStream_t stream);
+int launch_scan_backward(const ScanBackwardArgs& a, int dtype, int sms, cudaStream_t stream);
+int launch_scan_step(const ScanArgs& a, int dtype, cudaStream_t stream);
 
 }  // namespace gdn

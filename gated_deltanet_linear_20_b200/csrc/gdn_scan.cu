@@ -1,0 +1,506 @@
+// Channel recurrence (gated linear recurrence) with a parallel scan over time,
+// its single-token step and its backward pass.
+//
+//   forward   h_t   = alpha_t h_{t-1} + beta_t x_t,      alpha_t = exp(g_t)
+//   backward  lam_t = dh_t + alpha_{t+1} lam_{t+1},      lam_T = dh_T + dstate
+//             dx = beta lam, dbeta = x lam, dg = lam alpha_t h_{t-1},
+//             dh_0 = alpha_1 lam_1
+//
+// Every channel is a chain of its own, so the work is a stream over memory (one
+// exponential and a few multiply-adds an element): HBM bounds it.  Too few
+// chains to fill the GPU one thread each, so time is cut as well.  Over a run of
+// tokens the map from the state before it to the state behind it is affine,
+// c -> exp(G) c + H, with G the sum of the run's log decays and H its end state
+// from zero; the maps of neighbouring runs compose.
+//
+// A warp owns 32 V neighbouring channels of S consecutive tokens (a slice, held
+// in registers), the W warps of a CTA own consecutive slices, and the CTAs of a
+// cluster consecutive tiles of W S tokens; the cluster walks its sequence
+// cluster-tile by cluster-tile.  Per cluster-tile each thread (1) loads its
+// slice and finds its map, (2) leaves it in shared memory, where the CTA's map
+// is composed and sent to the other CTAs of the cluster, (3) applies the maps
+// before its own to the carried state and (4) walks its slice again from the
+// right state, writing results.  Each element is read once and written once,
+// no global memory carries partial results between CTAs, nothing is awaited but
+// hardware barriers, and the order of every sum is fixed: results do not
+// depend on timing.
+#include "gdn_internal.h"
+
+#include <algorithm>
+
+namespace gdn {
+namespace {
+
+constexpr int kCarryTokens = GDN_SCAN_CARRY_TOKENS;
+constexpr int kMaxWarps = 8;
+constexpr int kMaxCluster = 8;
+
+template <typename T, int V>
+struct alignas(sizeof(T) * V) Vec {
+  T v[V];
+};
+
+__device__ __forceinline__ float to_f(float x) { return x; }
+__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <typename T>
+__device__ __forceinline__ T from_f(float x);
+template <>
+__device__ __forceinline__ float from_f<float>(float x) {
+  return x;
+}
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) {
+  return __float2bfloat16(x);  // nearest even: the one rounding of a result
+}
+
+template <typename T, int V>
+__device__ __forceinline__ Vec<T, V> load(const T* p) {
+  return *reinterpret_cast<const Vec<T, V>*>(p);
+}
+template <typename T, int V>
+__device__ __forceinline__ void store(T* p, const float (&x)[V]) {
+  Vec<T, V> r;
+#pragma unroll
+  for (int e = 0; e < V; ++e) r.v[e] = from_f<T>(x[e]);
+  *reinterpret_cast<Vec<T, V>*>(p) = r;
+}
+
+// exp(G) c + H.  A state of exactly zero stays out of the product, so that runs
+// whose growth exp(G) overflows still start correctly from zero.
+__device__ __forceinline__ float apply(float2 m, float c) {
+  return c == 0.f ? m.y : fmaf(expf(m.x), c, m.y);
+}
+
+__device__ __forceinline__ unsigned cluster_size() {
+  unsigned n;
+  asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(n));
+  return n;
+}
+__device__ __forceinline__ unsigned cluster_rank() {
+  unsigned r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+// Stores a pair to the same shared-memory address in CTA `rank` of the cluster.
+__device__ __forceinline__ void store_remote(float2* local, unsigned rank, float2 v) {
+  unsigned a = static_cast<unsigned>(__cvta_generic_to_shared(local)), b;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(b) : "r"(a), "r"(rank));
+  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(b), "f"(v.x), "f"(v.y)
+               : "memory");
+}
+
+struct Seq {
+  long long start;  // first token
+  int len;
+  long long carry_row;
+};
+
+// The sequence `n` of the call; false if its packed offsets are invalid.
+__device__ __forceinline__ bool sequence(const ScanArgs& a, int n, Seq* s) {
+  if (!a.cu_seqlens) {
+    s->start = (long long)n * a.T;
+    s->len = a.T;
+    s->carry_row = (long long)n * ((a.T + kCarryTokens - 1) / kCarryTokens);
+    return true;
+  }
+  const int b = a.cu_seqlens[n], e = a.cu_seqlens[n + 1];
+  if (b < 0 || e < b || e > a.T) return false;
+  s->start = b;
+  s->len = e - b;
+  s->carry_row = b / kCarryTokens + n;
+  return true;
+}
+
+// Shared memory of the exchange: two sets, used in turn, so that one barrier a
+// cluster-tile is enough (a set is written again only behind the next one's).
+template <int V>
+struct Exchange {
+  float2 warp_map[2][kMaxWarps][32 * V];     // this CTA's slices, in scan order
+  float2 cta_map[2][kMaxCluster][32 * V];    // the cluster's tiles, in scan order
+};
+
+// Shares the map of this thread's slice (scan order: CTA `rank`, warp `w`) and
+// turns carry, the state before the cluster-tile, into the state before the
+// slice (returned in c) and the state behind the cluster-tile (carry).
+template <int V>
+__device__ __forceinline__ void scan_exchange(Exchange<V>& ex, int set, const float (&G)[V],
+                                              const float (&H)[V], float (&carry)[V],
+                                              float (&c)[V], int w, int W, int lane,
+                                              unsigned rank, unsigned n) {
+#pragma unroll
+  for (int e = 0; e < V; ++e) ex.warp_map[set][w][lane * V + e] = make_float2(G[e], H[e]);
+  __syncthreads();
+  if (n > 1) {
+    // warp w composes the CTA's map for the CTAs w, w + W, ...
+    if (w < n) {
+      float2 m[V];
+#pragma unroll
+      for (int e = 0; e < V; ++e) m[e] = ex.warp_map[set][0][lane * V + e];
+      for (int i = 1; i < W; ++i)
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          const float2 y = ex.warp_map[set][i][lane * V + e];
+          m[e] = make_float2(m[e].x + y.x, apply(y, m[e].y));
+        }
+      for (unsigned r = w; r < n; r += W)
+#pragma unroll
+        for (int e = 0; e < V; ++e) store_remote(&ex.cta_map[set][rank][lane * V + e], r, m[e]);
+    }
+    cluster_barrier();
+  }
+#pragma unroll
+  for (int e = 0; e < V; ++e) c[e] = carry[e];
+  if (n > 1) {
+    for (unsigned r = 0; r < n; ++r)
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        if (r == rank) c[e] = carry[e];
+        carry[e] = apply(ex.cta_map[set][r][lane * V + e], carry[e]);
+      }
+    for (int i = 0; i < w; ++i)
+#pragma unroll
+      for (int e = 0; e < V; ++e) c[e] = apply(ex.warp_map[set][i][lane * V + e], c[e]);
+  } else {
+    for (int i = 0; i < W; ++i)
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        if (i == w) c[e] = carry[e];
+        carry[e] = apply(ex.warp_map[set][i][lane * V + e], carry[e]);
+      }
+  }
+}
+
+template <typename T, int V, int S, bool BETA>
+__global__ void __launch_bounds__(32 * kMaxWarps, 2) scan_kernel(const ScanArgs a) {
+  __shared__ Exchange<V> ex;
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, W = blockDim.x >> 5;
+  const unsigned n = cluster_size(), rank = cluster_rank();
+  const int id = blockIdx.x / n, seq = id / a.cblocks;
+  const int c0 = (id % a.cblocks) * 32 * V + lane * V;
+  const bool on = c0 < a.C;
+  Seq s;
+  if (!sequence(a, seq, &s)) {  // the same answer in every CTA of the cluster
+    if (a.status && threadIdx.x == 0 && rank == 0) *a.status = GDN_ERR_SHAPE;
+    return;
+  }
+  if (n > 1) cluster_barrier();  // every CTA runs before its shared memory is written
+  float carry[V];
+#pragma unroll
+  for (int e = 0; e < V; ++e) carry[e] = 0.f;
+  if (a.h0 && on) {
+    const Vec<float, V> v = load<float, V>(a.h0 + (size_t)seq * a.C + c0);
+#pragma unroll
+    for (int e = 0; e < V; ++e) carry[e] = v.v[e];
+  }
+  const int tile = W * S, step = tile * int(n);
+  int set = 0;
+  for (int base = 0; base < s.len; base += step, set ^= 1) {
+    const int t0 = base + int(rank) * tile + w * S;
+    const int cnt = on ? min(max(s.len - t0, 0), S) : 0;
+    const size_t at = size_t(s.start + t0) * a.C + c0;
+    const T* px = static_cast<const T*>(a.x) + at;
+    const T* pb = static_cast<const T*>(a.beta) + at;
+    const float* pg = a.g + at;
+    Vec<float, V> g[S];
+    Vec<T, V> x[S], b[BETA ? S : 1];
+#pragma unroll
+    for (int i = 0; i < S; ++i)
+      if (i < cnt) {
+        g[i] = load<float, V>(pg + (size_t)i * a.C);
+        x[i] = load<T, V>(px + (size_t)i * a.C);
+        if (BETA) b[i] = load<T, V>(pb + (size_t)i * a.C);
+      }
+    float al[S][V], u[S][V], G[V], H[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) G[e] = H[e] = 0.f;
+#pragma unroll
+    for (int i = 0; i < S; ++i)
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        // tokens past the end (and channels past C) leave the state as it is
+        al[i][e] = i < cnt ? expf(g[i].v[e]) : 1.f;
+        u[i][e] = i < cnt ? to_f(x[i].v[e]) : 0.f;
+        if (BETA) u[i][e] *= i < cnt ? to_f(b[i].v[e]) : 0.f;
+        G[e] += i < cnt ? g[i].v[e] : 0.f;
+        H[e] = fmaf(al[i][e], H[e], u[i][e]);
+      }
+    float h[V];
+    scan_exchange<V>(ex, set, G, H, carry, h, w, W, lane, rank, n);
+    if (cnt > 0 && a.carries && t0 % kCarryTokens == 0)
+      store<float, V>(a.carries + size_t(s.carry_row + t0 / kCarryTokens) * a.C + c0, h);
+    if (a.h) {
+      T* ph = static_cast<T*>(a.h) + at;
+#pragma unroll
+      for (int i = 0; i < S; ++i)
+        if (i < cnt) {
+#pragma unroll
+          for (int e = 0; e < V; ++e) h[e] = fmaf(al[i][e], h[e], u[i][e]);
+          store<T, V>(ph + (size_t)i * a.C, h);
+        }
+    }
+  }
+  if (a.h_T && rank == 0 && w == 0 && on)
+    store<float, V>(a.h_T + (size_t)seq * a.C + c0, carry);
+}
+
+// Backward: the same walk from the sequence's end.  What passes a token
+// boundary is mu_t = alpha_t lam_t.  h_{t-1} is rebuilt in 32 bits from the
+// states that the forward pass kept every 16 tokens: reading them costs 4/16
+// byte an element, reading h itself 2 to 4 and, in bf16, its rounding in dg.
+template <typename T, int V, int S, bool BETA>
+__global__ void __launch_bounds__(32 * kMaxWarps, 2) scan_backward_kernel(const ScanBackwardArgs a) {
+  __shared__ Exchange<V> ex;
+  // the odd slices of a kept state's 16 tokens start from the slices before
+  constexpr int M = kCarryTokens / S;
+  __shared__ float2 fwd_map[M > 1 ? 2 : 1][M > 1 ? kMaxWarps : 1][32 * V];
+  const ScanArgs& f = a.f;
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, W = blockDim.x >> 5;
+  const unsigned n = cluster_size(), rank = cluster_rank();
+  const int id = blockIdx.x / n, seq = id / f.cblocks;
+  const int c0 = (id % f.cblocks) * 32 * V + lane * V;
+  const bool on = c0 < f.C;
+  Seq s;
+  if (!sequence(f, seq, &s)) {
+    if (f.status && threadIdx.x == 0 && rank == 0) *f.status = GDN_ERR_SHAPE;
+    return;
+  }
+  if (n > 1) cluster_barrier();
+  float carry[V];
+#pragma unroll
+  for (int e = 0; e < V; ++e) carry[e] = 0.f;
+  if (a.dh_T && on) {
+    const Vec<float, V> v = load<float, V>(a.dh_T + (size_t)seq * f.C + c0);
+#pragma unroll
+    for (int e = 0; e < V; ++e) carry[e] = v.v[e];
+  }
+  const int tile = W * S, tiles = (s.len + tile - 1) / tile;
+  int set = 0;
+  for (int first = 0; first < tiles; first += int(n), set ^= 1) {
+    // scan order runs backwards in time; a tile index below 0 is past the start
+    const int ti = tiles - 1 - first - int(rank);
+    const int sw = W - 1 - w;  // the slice of this warp within the tile
+    const int t0 = ti * tile + sw * S;
+    const int cnt = on && ti >= 0 ? min(max(s.len - t0, 0), S) : 0;
+    const size_t at = cnt > 0 ? size_t(s.start + t0) * f.C + c0 : 0;
+    Vec<float, V> g[S], hc;
+    Vec<T, V> x[S], b[BETA ? S : 1], d[S];
+#pragma unroll
+    for (int i = 0; i < S; ++i)
+      if (i < cnt) {
+        const size_t o = at + (size_t)i * f.C;
+        g[i] = load<float, V>(f.g + o);
+        d[i] = load<T, V>(static_cast<const T*>(a.dh) + o);
+        x[i] = load<T, V>(static_cast<const T*>(f.x) + o);
+        if (BETA) b[i] = load<T, V>(static_cast<const T*>(f.beta) + o);
+      }
+    if (cnt > 0)
+      hc = load<float, V>(f.carries + size_t(s.carry_row + t0 / kCarryTokens) * f.C + c0);
+    float al[S][V], G[V], R[V], H[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) G[e] = R[e] = H[e] = 0.f;
+#pragma unroll
+    for (int i = 0; i < S; ++i)
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        al[i][e] = i < cnt ? expf(g[i].v[e]) : 1.f;
+        G[e] += i < cnt ? g[i].v[e] : 0.f;
+        if (M > 1 && i < cnt) {
+          const float u = BETA ? to_f(x[i].v[e]) * to_f(b[i].v[e]) : to_f(x[i].v[e]);
+          H[e] = fmaf(al[i][e], H[e], u);
+        }
+      }
+#pragma unroll
+    for (int i = S - 1; i >= 0; --i)
+#pragma unroll
+      for (int e = 0; e < V; ++e)
+        if (i < cnt) R[e] = al[i][e] * (to_f(d[i].v[e]) + R[e]);
+    if (M > 1) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) fwd_map[set][sw][lane * V + e] = make_float2(G[e], H[e]);
+    }
+    float mu[V];
+    scan_exchange<V>(ex, set, G, R, carry, mu, w, W, lane, rank, n);
+    float hp[S][V];  // h before each token
+    if (cnt > 0) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        float h = hc.v[e];
+        if (M > 1)
+          for (int i = sw - sw % M; i < sw; ++i) h = apply(fwd_map[set][i][lane * V + e], h);
+#pragma unroll
+        for (int i = 0; i < S; ++i)
+          if (i < cnt) {
+            hp[i][e] = h;
+            const float u = BETA ? to_f(x[i].v[e]) * to_f(b[i].v[e]) : to_f(x[i].v[e]);
+            h = fmaf(al[i][e], h, u);
+          }
+      }
+#pragma unroll
+      for (int i = S - 1; i >= 0; --i)
+        if (i < cnt) {
+          float dx[V], db[V], dg[V];
+#pragma unroll
+          for (int e = 0; e < V; ++e) {
+            const float lam = to_f(d[i].v[e]) + mu[e];
+            mu[e] = al[i][e] * lam;
+            dg[e] = mu[e] * hp[i][e];
+            dx[e] = BETA ? lam * to_f(b[i].v[e]) : lam;
+            db[e] = lam * to_f(x[i].v[e]);
+          }
+          const size_t o = at + (size_t)i * f.C;
+          store<T, V>(static_cast<T*>(a.dx) + o, dx);
+          store<float, V>(a.dg + o, dg);
+          if (BETA) store<T, V>(static_cast<T*>(a.dbeta) + o, db);
+        }
+    }
+  }
+  if (a.dh0 && rank == 0 && w == 0 && on)
+    store<float, V>(a.dh0 + (size_t)seq * f.C + c0, carry);
+}
+
+// One token: elementwise, V channels a thread.
+template <typename T, int V, bool BETA>
+__global__ void __launch_bounds__(256) scan_step_kernel(const T* x, const float* g, const T* beta,
+                                                        float* state, T* h, size_t count) {
+  const size_t i = (size_t(blockIdx.x) * 256 + threadIdx.x) * V;
+  if (i >= count) return;
+  const Vec<T, V> vx = load<T, V>(x + i);
+  const Vec<float, V> vg = load<float, V>(g + i), vs = load<float, V>(state + i);
+  Vec<T, V> vb;
+  if (BETA) vb = load<T, V>(beta + i);
+  float r[V];
+#pragma unroll
+  for (int e = 0; e < V; ++e) {
+    const float u = BETA ? to_f(vx.v[e]) * to_f(vb.v[e]) : to_f(vx.v[e]);
+    r[e] = fmaf(expf(vg.v[e]), vs.v[e], u);
+  }
+  store<float, V>(state + i, r);
+  store<T, V>(h + i, r);
+}
+
+struct Shape {
+  int warps, cluster;
+};
+
+// Warps: enough for the sequence, at most 8.  Cluster: the fewest CTAs along
+// time that give every SM two CTAs, as long as each has tokens.
+Shape pick_shape(const ScanArgs& a, int S, int min_warps, long long chains, int sms) {
+  const long long avg = a.cu_seqlens ? std::max<long long>(1, a.T / std::max(1, a.N)) : a.T;
+  const long long slices = (avg + S - 1) / S;
+  int W = min_warps;
+  while (W < kMaxWarps && W < slices) W *= 2;
+  int n = 1;
+  while (n < kMaxCluster && chains * n < 2LL * sms && (long long)n * W < slices) n *= 2;
+  return {W, n};
+}
+
+template <typename Args>
+bool launch_cluster(void (*kernel)(const Args), const Args& args, long long ctas, Shape sh,
+                    cudaStream_t stream) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(unsigned(ctas * sh.cluster));
+  cfg.blockDim = dim3(unsigned(32 * sh.warps));
+  cfg.stream = stream;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = unsigned(sh.cluster);
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = sh.cluster > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, args) == cudaSuccess;
+}
+
+template <typename T, int V, int S>
+int run_scan(ScanArgs a, int sms, cudaStream_t stream) {
+  a.cblocks = (a.C + 32 * V - 1) / (32 * V);
+  const long long chains = (long long)a.cblocks * a.N;
+  if (chains * kMaxCluster > 0x7fffffffLL) return GDN_ERR_SHAPE;
+  const Shape sh = pick_shape(a, S, 1, chains, sms);
+  const bool ok = a.beta ? launch_cluster(&scan_kernel<T, V, S, true>, a, chains, sh, stream)
+                         : launch_cluster(&scan_kernel<T, V, S, false>, a, chains, sh, stream);
+  return ok ? GDN_OK : GDN_ERR_LAUNCH;
+}
+
+template <typename T, int V, int S>
+int run_backward(ScanBackwardArgs a, int sms, cudaStream_t stream) {
+  a.f.cblocks = (a.f.C + 32 * V - 1) / (32 * V);
+  const long long chains = (long long)a.f.cblocks * a.f.N;
+  if (chains * kMaxCluster > 0x7fffffffLL) return GDN_ERR_SHAPE;
+  const Shape sh = pick_shape(a.f, S, kCarryTokens / S, chains, sms);
+  const bool ok =
+      a.f.beta ? launch_cluster(&scan_backward_kernel<T, V, S, true>, a, chains, sh, stream)
+               : launch_cluster(&scan_backward_kernel<T, V, S, false>, a, chains, sh, stream);
+  return ok ? GDN_OK : GDN_ERR_LAUNCH;
+}
+
+// Two channels a thread where the channel count is even and every array starts
+// on a pair (4 bytes of bf16, 8 of fp32); else one.
+bool pairs_ok(const ScanArgs& a, int esize) {
+  const auto ok = [](const void* p, uintptr_t m) {
+    return (reinterpret_cast<uintptr_t>(p) & (m - 1)) == 0;
+  };
+  const uintptr_t e2 = 2 * uintptr_t(esize);
+  return a.C % 2 == 0 && ok(a.x, e2) && ok(a.beta, e2) && ok(a.h, e2) && ok(a.g, 8) &&
+         ok(a.h0, 8) && ok(a.h_T, 8) && ok(a.carries, 8);
+}
+
+}  // namespace
+
+int launch_scan(const ScanArgs& a, int dtype, int sms, cudaStream_t stream) {
+  const bool pairs = pairs_ok(a, dtype == GDN_BF16 ? 2 : 4);
+  if (dtype == GDN_BF16)
+    return pairs ? run_scan<__nv_bfloat16, 2, 16>(a, sms, stream)
+                 : run_scan<__nv_bfloat16, 1, 16>(a, sms, stream);
+  return pairs ? run_scan<float, 2, 8>(a, sms, stream) : run_scan<float, 1, 16>(a, sms, stream);
+}
+
+int launch_scan_backward(const ScanBackwardArgs& a, int dtype, int sms, cudaStream_t stream) {
+  const int esize = dtype == GDN_BF16 ? 2 : 4;
+  ScanArgs o{};  // the arrays of the backward pass alone, for the same rule
+  o.C = a.f.C;
+  o.x = a.dh;
+  o.beta = a.dx;
+  o.h = a.dbeta;
+  o.g = a.dg;
+  o.h0 = a.dh_T;
+  o.h_T = a.dh0;
+  const bool pairs = pairs_ok(a.f, esize) && pairs_ok(o, esize);
+  if (dtype == GDN_BF16)
+    return pairs ? run_backward<__nv_bfloat16, 2, 8>(a, sms, stream)
+                 : run_backward<__nv_bfloat16, 1, 16>(a, sms, stream);
+  return pairs ? run_backward<float, 2, 8>(a, sms, stream)
+               : run_backward<float, 1, 16>(a, sms, stream);
+}
+
+template <typename T, int V>
+static int run_step(const ScanArgs& a, size_t count, cudaStream_t stream) {
+  const unsigned grid = unsigned((count / V + 255) / 256);
+  const T *x = static_cast<const T*>(a.x), *b = static_cast<const T*>(a.beta);
+  if (a.beta)
+    scan_step_kernel<T, V, true><<<grid, 256, 0, stream>>>(x, a.g, b, a.h_T, static_cast<T*>(a.h),
+                                                           count);
+  else
+    scan_step_kernel<T, V, false><<<grid, 256, 0, stream>>>(x, a.g, b, a.h_T, static_cast<T*>(a.h),
+                                                            count);
+  return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_LAUNCH;
+}
+
+int launch_scan_step(const ScanArgs& a, int dtype, cudaStream_t stream) {
+  const size_t count = size_t(a.N) * a.C;
+  const auto ok = [](const void* p, uintptr_t m) {
+    return (reinterpret_cast<uintptr_t>(p) & (m - 1)) == 0;
+  };
+  const uintptr_t e4 = dtype == GDN_BF16 ? 8 : 16;
+  const bool quads = count % 4 == 0 && ok(a.x, e4) && ok(a.beta, e4) && ok(a.h, e4) &&
+                     ok(a.g, 16) && ok(a.h_T, 16);
+  if (dtype == GDN_BF16)
+    return quads ? run_step<__nv_bfloat16, 4>(a, count, stream)
+                 : run_step<__nv_bfloat16, 1>(a, count, stream);
+  return quads ? run_step<float, 4>(a, count, stream) : run_step<float, 1>(a, count, stream);
+}
+
+}  // namespace gdn

@@ -1,0 +1,227 @@
+"""Channel recurrence (gated linear recurrence): binding of the gdn_scan calls.
+
+    h_t = exp(g_t) h_{t-1} + beta_t x_t        per sequence and channel
+
+Argument marshalling only, as in ``gdn.py``: the arithmetic is in the library's
+CUDA kernels.  ``scan`` / ``scan_varlen`` run whole sequences, ``scan_step`` one
+token with the state in place, and the ``*_backward`` calls return gradients.
+Calls run on the current stream of the tensors' device.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Optional
+
+import torch
+
+from .gdn import GDN_OK, GDNError, _check, _lib
+
+_vp, _ci = ctypes.c_void_p, ctypes.c_int
+for _name, _args in (("gdn_scan", [_vp] * 7 + [_ci] * 4 + [_vp]),
+                     ("gdn_scan_varlen", [_vp] * 8 + [_ci] * 4 + [_vp, _vp]),
+                     ("gdn_scan_step", [_vp] * 5 + [_ci] * 3 + [_vp]),
+                     ("gdn_scan_backward", [_vp] * 11 + [_ci] * 5 + [_vp]),
+                     ("gdn_scan_varlen_backward", [_vp] * 11 + [_ci, _vp] + [_ci] * 4 + [_vp, _vp])):
+    getattr(_lib, _name).argtypes = _args
+    getattr(_lib, _name).restype = _ci
+_lib.gdn_scan_carry_bytes.argtypes = [_ci] * 4
+_lib.gdn_scan_carry_bytes.restype = ctypes.c_size_t
+
+CARRY_TOKENS = 16  # GDN_SCAN_CARRY_TOKENS
+DTYPES = {torch.float32: 0, torch.bfloat16: 1}  # gdn_dtype
+_F32, _I32 = torch.float32, torch.int32
+
+
+def _expect(t, name, dtype, shape, device):
+    """_check with its common answer first: the calls of one token are short."""
+    if type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape and t.device == device \
+            and t.is_contiguous():
+        return t.data_ptr()
+    _check(t, name, dtype, shape, device)
+    return t.data_ptr()
+
+
+def _optional(t, name, dtype, shape, device):
+    return None if t is None else _expect(t, name, dtype, shape, device)
+
+
+def _device(t: torch.Tensor, what: str) -> torch.device:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("x must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{what} runs on CUDA tensors only (no CPU path)")
+    return t.device
+
+
+def _dtype(t: torch.Tensor, name: str) -> int:
+    code = DTYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be torch.float32 or torch.bfloat16, got {t.dtype}")
+    return code
+
+
+def _call(name: str, device: torch.device, *args):
+    """Calls the library on the tensors' device and its current stream."""
+    fn = getattr(_lib, name)
+    stream = torch.cuda.current_stream(device).cuda_stream
+    if torch.cuda.current_device() == device.index:
+        rc = fn(*args, stream)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, stream)
+    if rc != GDN_OK:
+        raise GDNError(rc, name)
+
+
+def _out(t, name, dtype, shape, device):
+    """A given output, checked, or a new one."""
+    if t is None:
+        t = torch.empty(shape, dtype=dtype, device=device)
+    else:
+        _check(t, name, dtype, shape, device)
+    return t
+
+
+def _carry_shape(N: int, tokens: int, C: int, packed: bool):
+    if packed:
+        return (tokens // CARRY_TOKENS + N, C)
+    return (N, -(-(tokens // N if N else 0) // CARRY_TOKENS), C)
+
+
+def scan(x: torch.Tensor, g: torch.Tensor, beta: Optional[torch.Tensor] = None,
+         h0: Optional[torch.Tensor] = None, *, h: Optional[torch.Tensor] = None,
+         h_T: Optional[torch.Tensor] = None, save_carries: bool = False):
+    """The recurrence over B sequences of T tokens: returns (h [B,T,C], h_T [B,C] fp32).
+
+    x, beta [B,T,C] fp32 or bf16 (beta None: 1); g [B,T,C] fp32 natural-log
+    decays; h0 [B,C] fp32 or None (zeros).  h has x's type.  ``h`` / ``h_T`` may
+    be given preallocated (``h_T`` may be ``h0``).  ``save_carries`` also returns
+    the states before every 16th token ([B, ceil(T/16), C] fp32), which
+    ``scan_backward`` takes."""
+    dev = _device(x, "scan")
+    if x.dim() != 3:
+        raise ValueError("x must be [B,T,C]")
+    shape = x.shape
+    B, T, C = shape
+    dt = _dtype(x, "x")
+    px = _expect(x, "x", x.dtype, shape, dev)
+    pg = _expect(g, "g", _F32, shape, dev)
+    pb = _optional(beta, "beta", x.dtype, shape, dev)
+    p0 = _optional(h0, "h0", _F32, (B, C), dev)
+    h = _out(h, "h", x.dtype, shape, dev)
+    h_T = _out(h_T, "h_T", _F32, (B, C), dev)
+    carries = torch.empty(_carry_shape(B, B * T, C, False), dtype=_F32, device=dev) \
+        if save_carries else None
+    _call("gdn_scan", dev, px, pg, pb, p0, h.data_ptr(), h_T.data_ptr(),
+          None if carries is None else carries.data_ptr(), B, T, C, dt)
+    return (h, h_T, carries) if save_carries else (h, h_T)
+
+
+def _packed(x, cu_seqlens, status, dev):
+    if x.dim() != 2:
+        raise ValueError("x must be [total_T,C]")
+    if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+        raise ValueError("cu_seqlens must be [N+1]")
+    N = cu_seqlens.numel() - 1
+    return (N, _expect(cu_seqlens, "cu_seqlens", _I32, (N + 1,), dev),
+            _optional(status, "status", _I32, (1,), dev))
+
+
+def scan_varlen(x: torch.Tensor, g: torch.Tensor, cu_seqlens: torch.Tensor,
+                beta: Optional[torch.Tensor] = None, h0: Optional[torch.Tensor] = None, *,
+                h: Optional[torch.Tensor] = None, h_T: Optional[torch.Tensor] = None,
+                save_carries: bool = False, status: Optional[torch.Tensor] = None):
+    """``scan`` of N packed sequences: x, g, beta [total_T,C], cu_seqlens int32
+    [N+1] on the device, h0 [N,C]; returns (h [total_T,C], h_T [N,C] fp32), and
+    with ``save_carries`` the kept states ([total_T // 16 + N, C] fp32)."""
+    dev = _device(x, "scan_varlen")
+    N, pcu, pst = _packed(x, cu_seqlens, status, dev)
+    shape = x.shape
+    T, C = shape
+    dt = _dtype(x, "x")
+    px = _expect(x, "x", x.dtype, shape, dev)
+    pg = _expect(g, "g", _F32, shape, dev)
+    pb = _optional(beta, "beta", x.dtype, shape, dev)
+    p0 = _optional(h0, "h0", _F32, (N, C), dev)
+    h = _out(h, "h", x.dtype, shape, dev)
+    h_T = _out(h_T, "h_T", _F32, (N, C), dev)
+    carries = torch.empty(_carry_shape(N, T, C, True), dtype=_F32, device=dev) \
+        if save_carries else None
+    _call("gdn_scan_varlen", dev, px, pg, pb, p0, h.data_ptr(), h_T.data_ptr(),
+          None if carries is None else carries.data_ptr(), pcu, N, T, C, dt, pst)
+    return (h, h_T, carries) if save_carries else (h, h_T)
+
+
+def scan_step(x: torch.Tensor, g: torch.Tensor, state: torch.Tensor,
+              beta: Optional[torch.Tensor] = None, *,
+              h: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """One token of B sequences; ``state`` [B,C] fp32 is updated in place.
+    Returns h [B,C], the new state in x's type.
+
+    x, beta [B,C] fp32 or bf16 (beta None: 1); g [B,C] fp32."""
+    dev = _device(x, "scan_step")
+    if x.dim() != 2:
+        raise ValueError("x must be [B,C]")
+    shape = x.shape
+    B, C = shape
+    dt = _dtype(x, "x")
+    px = _expect(x, "x", x.dtype, shape, dev)
+    pg = _expect(g, "g", _F32, shape, dev)
+    ps = _expect(state, "state", _F32, shape, dev)
+    pb = _optional(beta, "beta", x.dtype, shape, dev)
+    h = _out(h, "h", x.dtype, shape, dev)
+    _call("gdn_scan_step", dev, px, pg, pb, ps, h.data_ptr(), B, C, dt)
+    return h
+
+
+def _backward(name, dh, x, g, beta, h0, dh_T, carries, N, tokens, packed, sizes,
+              tail, dev):
+    shape, C = x.shape, x.shape[-1]
+    dt = _dtype(x, "x")
+    px = _expect(x, "x", x.dtype, shape, dev)
+    pg = _expect(g, "g", _F32, shape, dev)
+    pb = _optional(beta, "beta", x.dtype, shape, dev)
+    p0 = _optional(h0, "h0", _F32, (N, C), dev)
+    pdh = _expect(dh, "dh", x.dtype, shape, dev)
+    pdt = _optional(dh_T, "dh_T", _F32, (N, C), dev)
+    kept = carries is not None
+    carries = _out(carries, "carries", _F32, _carry_shape(N, tokens, C, packed), dev)
+    dx = torch.empty_like(x)
+    dg = torch.empty_like(g)
+    dbeta = torch.empty_like(beta) if beta is not None else None
+    dh0 = torch.empty_like(h0) if h0 is not None else None
+    _call(name, dev, px, pg, pb, p0, pdh, pdt, dx.data_ptr(), dg.data_ptr(),
+          None if dbeta is None else dbeta.data_ptr(), None if dh0 is None else dh0.data_ptr(),
+          carries.data_ptr(), int(kept), *sizes, C, dt, *tail)
+    return dx, dg, dbeta, dh0
+
+
+def scan_backward(dh: torch.Tensor, x: torch.Tensor, g: torch.Tensor,
+                  beta: Optional[torch.Tensor] = None, h0: Optional[torch.Tensor] = None,
+                  dh_T: Optional[torch.Tensor] = None, *, carries: Optional[torch.Tensor] = None):
+    """Gradients of ``scan``'s inputs: returns (dx, dg, dbeta, dh0), dbeta and dh0
+    None where beta and h0 are.
+
+    dh [B,T,C] has x's type, dh_T [B,C] fp32 or None (zeros).  ``carries`` is what
+    ``scan(..., save_carries=True)`` returned for the same inputs; without it the
+    states are computed again first."""
+    dev = _device(x, "scan_backward")
+    if x.dim() != 3:
+        raise ValueError("x must be [B,T,C]")
+    B, T, _ = x.shape
+    return _backward("gdn_scan_backward", dh, x, g, beta, h0, dh_T, carries, B, B * T, False,
+                     (B, T), (), dev)
+
+
+def scan_varlen_backward(dh: torch.Tensor, x: torch.Tensor, g: torch.Tensor,
+                         cu_seqlens: torch.Tensor, beta: Optional[torch.Tensor] = None,
+                         h0: Optional[torch.Tensor] = None, dh_T: Optional[torch.Tensor] = None, *,
+                         carries: Optional[torch.Tensor] = None,
+                         status: Optional[torch.Tensor] = None):
+    """Gradients of ``scan_varlen``'s inputs, as ``scan_backward``.  Gradients of
+    tokens behind the last sequence are not written."""
+    dev = _device(x, "scan_varlen_backward")
+    N, pcu, pst = _packed(x, cu_seqlens, status, dev)
+    T = x.shape[0]
+    return _backward("gdn_scan_varlen_backward", dh, x, g, beta, h0, dh_T, carries, N, T, True,
+                     (pcu, N, T), (pst,), dev)

@@ -379,6 +379,86 @@ int gdn_kda_prefill_varlen_ex(const void* q, const void* k, const void* v, const
                               float* snaps, int snap_every, int n_snaps,
                               const gdn_options* opts, int* status, void* stream);
 
+/* Element type of the activations of the calls below. */
+enum gdn_dtype { GDN_F32 = 0, GDN_BF16 = 1 };
+
+/* Tokens between the states that gdn_scan keeps for its backward pass. */
+#define GDN_SCAN_CARRY_TOKENS 16
+
+/* Channel recurrence (gated linear recurrence): for every sequence and channel
+ *     h_t = exp(g_t) h_{t-1} + beta_t x_t,   t = 1 .. T,  h_0 given or zero.
+ * The vector-state companion of the gated delta rule; its gates follow the
+ * same conventions (g the natural log of the decay, one per token and channel
+ * as in the per-channel-gate calls; g > 0 is accepted and grows the state).
+ *   x, beta, h : [B][T][C], fp32 or bf16 by `dtype`; beta NULL means 1
+ *   g          : [B][T][C] fp32
+ *   h0, h_T    : [B][C] fp32; h0 NULL means zeros; h_T is written and may be h0
+ *   carries    : optional fp32 output (NULL: none) of gdn_scan_carry_bytes(B,
+ *                B*T, C, 0) bytes, kept for gdn_scan_backward: the state before
+ *                token 16 j + 1 of sequence b, at [b][j][C], j = 0 ..
+ *                ceil(T / 16) - 1
+ * The recurrence is computed in fp32 and rounded once, in h.  Runs of tokens
+ * are walked in parallel and joined exactly up to rounding, as long as the
+ * growth exp(sum of g) over 1024 consecutive tokens stays in the fp32 range.
+ * Results do not depend on timing (bitwise repeatable on the same device).
+ * B*C == 0 is a no-op; T == 0 writes h_T = h0 (or zeros).  Arrays need the
+ * alignment of their element type; offsets are 64-bit: B*T up to 2^30 tokens.
+ * Returns GDN_OK after enqueueing, GDN_ERR_NULL, GDN_ERR_ALIGN, GDN_ERR_SHAPE
+ * (negative or too large), GDN_ERR_UNSUPPORTED (dtype, device), GDN_ERR_ALIAS
+ * (an output overlaps an input or another output, except h_T == h0) or
+ * GDN_ERR_LAUNCH. */
+int gdn_scan(const void* x, const float* g, const void* beta, const float* h0, void* h, float* h_T,
+             float* carries, int B, int T, int C, int dtype, void* stream);
+
+/* gdn_scan of N sequences packed along the token axis, as in
+ * gdn_prefill_varlen: x, g, beta, h [total_T][C], h0, h_T [N][C], cu_seqlens
+ * device int[N+1].  Offsets that are out of order or outside 0 .. total_T are
+ * detected on the device: GDN_ERR_SHAPE goes to *status (if non-NULL) and that
+ * sequence's outputs are not written.  Empty sequences give h_T = h0 (or
+ * zeros).  Tokens of h behind the last sequence stay as they were.
+ *   carries : gdn_scan_carry_bytes(N, total_T, C, 1) bytes; sequence n's states
+ *             begin at row cu_seqlens[n] / 16 + n; rows between are not written */
+int gdn_scan_varlen(const void* x, const float* g, const void* beta, const float* h0, void* h,
+                    float* h_T, float* carries, const int* cu_seqlens, int N, int total_T, int C,
+                    int dtype, int* status, void* stream);
+
+/* Bytes of `carries` for N sequences of `tokens` tokens in all (equal lengths,
+ * or packed: nonzero `packed`); 0 for negative sizes. */
+size_t gdn_scan_carry_bytes(int N, int tokens, int C, int packed);
+
+/* One token of B sequences, the state updated in place:
+ *   h = state = exp(g) state + beta x;  x, beta, h [B][C] by `dtype` (beta NULL:
+ * 1), g, state [B][C] fp32.  Alignment, aliasing and errors as for gdn_scan. */
+int gdn_scan_step(const void* x, const float* g, const void* beta, float* state, void* h, int B,
+                  int C, int dtype, void* stream);
+
+/* Gradients of gdn_scan's inputs, given those of its outputs:
+ *     lam_t = dh_t + exp(g_{t+1}) lam_{t+1},  lam_T = dh_T-th token + dh_T
+ *     dx = beta lam, dbeta = x lam, dg = lam exp(g_t) h_{t-1}, dh0 = exp(g_1) lam_1
+ *   x, g, beta, h0 : the forward call's inputs
+ *   dh       : [B][T][C] by `dtype`;  dh_T [B][C] fp32 or NULL (zeros)
+ *   dx, dbeta: [B][T][C] by `dtype`, written; dbeta is needed exactly if beta is given
+ *   dg       : [B][T][C] fp32, written
+ *   dh0      : [B][C] fp32, written, or NULL (not wanted); may be dh_T
+ *   carries  : gdn_scan_carry_bytes bytes.  With carries_valid nonzero it holds
+ *              what gdn_scan left there for the same inputs and is only read;
+ *              with zero it is scratch that the call fills first (a second
+ *              launch that reads x, g and beta once more).  Two calls in flight
+ *              must not share scratch.
+ * Sums and states are fp32; h is rebuilt in fp32, not read back rounded.
+ * Sizes, alignment, errors and repeatability as for gdn_scan. */
+int gdn_scan_backward(const void* x, const float* g, const void* beta, const float* h0,
+                      const void* dh, const float* dh_T, void* dx, float* dg, void* dbeta,
+                      float* dh0, float* carries, int carries_valid, int B, int T, int C,
+                      int dtype, void* stream);
+
+/* gdn_scan_backward of packed sequences (gdn_scan_varlen).  An invalid
+ * sequence's gradients are not written. */
+int gdn_scan_varlen_backward(const void* x, const float* g, const void* beta, const float* h0,
+                             const void* dh, const float* dh_T, void* dx, float* dg, void* dbeta,
+                             float* dh0, float* carries, int carries_valid, const int* cu_seqlens,
+                             int N, int total_T, int C, int dtype, int* status, void* stream);
+
 /* Synchronises `stream`, then reads the device status word written by the
  * kernels.  Returns the word (GDN_OK, GDN_ERR_DEVICE_TIMEOUT, or GDN_ERR_SHAPE
  * from the packed-sequence calls), GDN_ERR_NULL (status_dev is NULL) or
