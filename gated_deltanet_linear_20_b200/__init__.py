@@ -24,15 +24,19 @@ from __future__ import annotations
 __all__ = ["prefill", "decode_step", "decode_tokens", "prefill_varlen", "kda_prefill",
            "kda_prefill_varlen", "kda_decode", "abi_version", "status_str", "query_status",
            "GDNError", "scan", "scan_varlen", "scan_step", "scan_backward",
-           "scan_varlen_backward"]
+           "scan_varlen_backward", "gated_norm", "gated_norm_backward", "residual_norm",
+           "residual_norm_backward"]
 
-_RECURRENCE = ("scan", "scan_varlen", "scan_step", "scan_backward", "scan_varlen_backward")
+_MODULES = {**dict.fromkeys(("scan", "scan_varlen", "scan_step", "scan_backward",
+                             "scan_varlen_backward"), ".recurrence"),
+            **dict.fromkeys(("gated_norm", "gated_norm_backward", "residual_norm",
+                             "residual_norm_backward"), ".norms")}
 
 
 def __getattr__(name):
-    if name in _RECURRENCE:
+    if name in _MODULES:
         import importlib
-        value = getattr(importlib.import_module(__name__ + ".recurrence"), name)
+        value = getattr(importlib.import_module(__name__ + _MODULES[name]), name)
         globals()[name] = value  # later uses find it without this function
         return value
     if name in ("prefill", "decode_step", "decode_tokens", "prefill_varlen", "kda_prefill",

@@ -125,6 +125,46 @@ struct ScanBackwardArgs {
   float* dh0;            // [N][C] or null (not wanted)
 };
 
+// Norm of a row times its gate, and its gradients (w holds D weights).
+struct GatedNormArgs {
+  const void* x;   // [rows][D]
+  const void* z;   // [rows][D] or null (no gate)
+  const float* w;  // [D]
+  void* y;
+  long long rows;
+  int D, act;      // act: gdn_gate
+  float eps, offset;
+  const void* dy;
+  void* dx;
+  void* dz;        // null without z
+  float* dw;
+  float* part;     // partial sums of dw: one row of D per CTA
+};
+// The step between two blocks, and its gradients.
+struct ResidualNormArgs {
+  const void* x;        // [rows][D], the block's output
+  const void* r;        // [rows][D], the residual stream; backward: the kept sum
+  const void* z;        // or null
+  const float* w;
+  const float* w_post;  // or null (no norm behind the block)
+  const float* scale;   // or null (1)
+  void* y;
+  void* r_out;
+  long long rows;
+  int D, act;
+  float eps, offset;
+  const void* dy;
+  const void* dr_out;   // or null (zeros)
+  void* dx;
+  void* dr;
+  void* dz;
+  float* dw;
+  float* dw_post;
+  float* dscale;
+  float* part;          // per CTA one row of D for each of the `weights` weights
+  int weights;
+};
+
 // Sets the dynamic shared-memory limit of `func` to `bytes` once per device
 // (slot: a small per-kernel index); returns false if the attribute call failed.
 bool ensure_smem_attr(const void* func, int slot, int bytes);
@@ -155,5 +195,22 @@ bool rows_head_dims_ok(int Dk, int Dv);
 int launch_scan(const ScanArgs& a, int dtype, int sms, cudaStream_t stream);
 int launch_scan_backward(const ScanBackwardArgs& a, int dtype, int sms, cudaStream_t stream);
 int launch_scan_step(const ScanArgs& a, int dtype, cudaStream_t stream);
+
+// The most CTAs of a norm's backward launch: each leaves one partial sum of each
+// weight gradient.  Four or (CTAs of one row) two per SM of a B200.
+constexpr int kNormMaxD = 16384;
+inline int norm_max_parts(long long rows, int D) {
+  const long long most = D <= 256 ? 592 : 296;
+  return int(rows < most ? rows : most);
+}
+
+// Norms: GDN_OK or a negative code; types GDN_F32 or GDN_BF16.
+int launch_gated_norm(const GatedNormArgs& a, int x_dtype, int dtype, int sms, cudaStream_t stream);
+int launch_gated_norm_backward(const GatedNormArgs& a, int x_dtype, int dtype, int sms,
+                               cudaStream_t stream);
+int launch_residual_norm(const ResidualNormArgs& a, int dtype, int r_dtype, int sms,
+                         cudaStream_t stream);
+int launch_residual_norm_backward(const ResidualNormArgs& a, int dtype, int r_dtype, int sms,
+                                  cudaStream_t stream);
 
 }  // namespace gdn

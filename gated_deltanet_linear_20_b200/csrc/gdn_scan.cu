@@ -24,9 +24,10 @@
 // no global memory carries partial results between CTAs, nothing is awaited but
 // hardware barriers, and the order of every sum is fixed: results do not
 // depend on timing.
-#include "gdn_internal.h"
-
 #include <algorithm>
+
+#include "gdn_internal.h"
+#include "gdn_vec.cuh"
 
 namespace gdn {
 namespace {
@@ -34,36 +35,6 @@ namespace {
 constexpr int kCarryTokens = GDN_SCAN_CARRY_TOKENS;
 constexpr int kMaxWarps = 8;
 constexpr int kMaxCluster = 8;
-
-template <typename T, int V>
-struct alignas(sizeof(T) * V) Vec {
-  T v[V];
-};
-
-__device__ __forceinline__ float to_f(float x) { return x; }
-__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
-template <typename T>
-__device__ __forceinline__ T from_f(float x);
-template <>
-__device__ __forceinline__ float from_f<float>(float x) {
-  return x;
-}
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) {
-  return __float2bfloat16(x);  // nearest even: the one rounding of a result
-}
-
-template <typename T, int V>
-__device__ __forceinline__ Vec<T, V> load(const T* p) {
-  return *reinterpret_cast<const Vec<T, V>*>(p);
-}
-template <typename T, int V>
-__device__ __forceinline__ void store(T* p, const float (&x)[V]) {
-  Vec<T, V> r;
-#pragma unroll
-  for (int e = 0; e < V; ++e) r.v[e] = from_f<T>(x[e]);
-  *reinterpret_cast<Vec<T, V>*>(p) = r;
-}
 
 // exp(G) c + H.  A state of exactly zero stays out of the product, so that runs
 // whose growth exp(G) overflows still start correctly from zero.

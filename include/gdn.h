@@ -459,6 +459,71 @@ int gdn_scan_varlen_backward(const void* x, const float* g, const void* beta, co
                              float* dh0, float* carries, int carries_valid, const int* cu_seqlens,
                              int N, int total_T, int C, int dtype, int* status, void* stream);
 
+/* The norms around a layer.  Gates and options:
+ *   size          : sizeof(gdn_norm_options)
+ *   eps           : added to the mean square, finite, >= 0
+ *   weight_offset : added to every norm weight (1 for weights kept around zero)
+ *   gate          : GDN_GATE_SILU a(z) = z / (1 + exp(-z)), or GDN_GATE_SIGMOID
+ * NULL options mean eps = 1e-6, weight_offset = 0, the SiLU gate; invalid ones
+ * are GDN_ERR_UNSUPPORTED.  In all four calls rows have D <= 16384 channels
+ * (GDN_ERR_SHAPE above), weights and their gradients are fp32 [D], squares and
+ * sums fp32, and each result is rounded once; arrays need the alignment of
+ * their element type (16 bytes and D a multiple of 8 give the widest accesses);
+ * rows == 0 or D == 0 writes no rows (weight gradients become zero).  Results
+ * are bitwise repeatable.  Errors otherwise as for gdn_scan. */
+enum gdn_gate { GDN_GATE_SILU = 0, GDN_GATE_SIGMOID = 1 };
+typedef struct gdn_norm_options {
+  int size;
+  float eps;
+  float weight_offset;
+  int gate;
+} gdn_norm_options;
+
+/* RMS norm of each row times a gate, e.g. of o [B][T][H][Dv] per head
+ * (rows = B*T*H, D = Dv), or a plain norm with z NULL:
+ *     y = a(z) w x / sqrt(mean(x^2) + eps)
+ *   x    : [rows][D] by `x_dtype` (o is fp32, or bf16 with o_bf16)
+ *   z, y : [rows][D] by `dtype`; z NULL: no gate;  w : [D] */
+int gdn_gated_norm(const void* x, int x_dtype, const float* w, const void* z, void* y, int rows,
+                   int D, int dtype, const gdn_norm_options* opts, void* stream);
+
+/* Its gradients: dx (by x_dtype), dz (by dtype; needed exactly if z is given)
+ * and dw = the sum over rows.  workspace: gdn_norm_workspace_bytes(rows, D, 1)
+ * bytes, 256-byte aligned, contents irrelevant; two calls in flight must not
+ * share it (GDN_ERR_WORKSPACE if NULL, misaligned or too small). */
+int gdn_gated_norm_backward(const void* dy, const void* x, int x_dtype, const float* w,
+                            const void* z, void* dx, void* dz, float* dw, int rows, int D,
+                            int dtype, void* workspace, size_t workspace_bytes,
+                            const gdn_norm_options* opts, void* stream);
+
+/* The step between two blocks: norm behind the block, gate and scale, the
+ * residual sum, and the norm before the next block:
+ *     u = w_post x / rms(x)  (x itself without w_post)
+ *     r_out = r + scale a(z) u        y = w r_out / rms(r_out)
+ *   x, z, y  : [rows][D] by `dtype`; z NULL: no gate
+ *   r, r_out : [rows][D] by `r_dtype`, no narrower than dtype (else
+ *              GDN_ERR_UNSUPPORTED); r_out may be r
+ *   w, w_post, scale : [D]; w_post NULL: no norm behind the block; scale NULL: 1
+ * y is computed from the sum before it is rounded to r_dtype. */
+int gdn_residual_norm(const void* x, const void* r, const float* w, const void* z,
+                      const float* w_post, const float* scale, void* y, void* r_out, int rows,
+                      int D, int dtype, int r_dtype, const gdn_norm_options* opts, void* stream);
+
+/* Its gradients at the kept sum r_out, given dy and dr_out (NULL: zeros): dx, dr
+ * (dr may be dr_out), dz, dw, dw_post and dscale, each needed exactly if its
+ * input is given.  workspace as for gdn_gated_norm_backward, with `weights` the
+ * number of weight arrays given (w, w_post, scale). */
+int gdn_residual_norm_backward(const void* dy, const void* dr_out, const void* x,
+                               const void* r_out, const float* w, const void* z,
+                               const float* w_post, const float* scale, void* dx, void* dr,
+                               void* dz, float* dw, float* dw_post, float* dscale, int rows, int D,
+                               int dtype, int r_dtype, void* workspace, size_t workspace_bytes,
+                               const gdn_norm_options* opts, void* stream);
+
+/* Workspace of a norm's backward call with 1 to 3 weight arrays; 0 for invalid
+ * sizes or no rows. */
+size_t gdn_norm_workspace_bytes(int rows, int D, int weights);
+
 /* Synchronises `stream`, then reads the device status word written by the
  * kernels.  Returns the word (GDN_OK, GDN_ERR_DEVICE_TIMEOUT, or GDN_ERR_SHAPE
  * from the packed-sequence calls), GDN_ERR_NULL (status_dev is NULL) or
