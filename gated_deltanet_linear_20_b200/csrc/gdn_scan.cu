@@ -33,13 +33,21 @@ namespace gdn {
 namespace {
 
 constexpr int kCarryTokens = GDN_SCAN_CARRY_TOKENS;
-constexpr int kMaxWarps = 8;
-constexpr int kMaxCluster = 8;
+constexpr int kWarps = 4;       // of a CTA, along time
+constexpr int kMaxCluster = 8;  // CTAs along time
 
-// exp(G) c + H.  A state of exactly zero stays out of the product, so that runs
-// whose growth exp(G) overflows still start correctly from zero.
-__device__ __forceinline__ float apply(float2 m, float c) {
-  return c == 0.f ? m.y : fmaf(expf(m.x), c, m.y);
+// The map of a run of tokens for V channels: c -> A c + H.  A stays finite, so
+// that a state of zero stays out of a run whose growth passes the fp32 range.
+template <int V>
+struct alignas(8 * V) Map {
+  float A[V], H[V];
+};
+__device__ __forceinline__ float finite(float a) { return fminf(a, 3.402823466e38f); }
+
+template <int V>
+__device__ __forceinline__ void apply(const Map<V>& m, float (&c)[V]) {
+#pragma unroll
+  for (int e = 0; e < V; ++e) c[e] = fmaf(m.A[e], c[e], m.H[e]);
 }
 
 __device__ __forceinline__ unsigned cluster_size() {
@@ -56,12 +64,18 @@ __device__ __forceinline__ void cluster_barrier() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
                    : "memory");
 }
-// Stores a pair to the same shared-memory address in CTA `rank` of the cluster.
-__device__ __forceinline__ void store_remote(float2* local, unsigned rank, float2 v) {
+// Stores a map to the same shared-memory address in CTA `rank` of the cluster.
+template <int V>
+__device__ __forceinline__ void store_remote(Map<V>* local, unsigned rank, const Map<V>& m) {
   unsigned a = static_cast<unsigned>(__cvta_generic_to_shared(local)), b;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(b) : "r"(a), "r"(rank));
-  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(b), "f"(v.x), "f"(v.y)
-               : "memory");
+  if constexpr (V == 2)
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(b), "f"(m.A[0]),
+                 "f"(m.A[1]), "f"(m.H[0]), "f"(m.H[1])
+                 : "memory");
+  else
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(b), "f"(m.A[0]), "f"(m.H[0])
+                 : "memory");
 }
 
 struct Seq {
@@ -90,69 +104,84 @@ __device__ __forceinline__ bool sequence(const ScanArgs& a, int n, Seq* s) {
 // cluster-tile is enough (a set is written again only behind the next one's).
 template <int V>
 struct Exchange {
-  float2 warp_map[2][kMaxWarps][32 * V];     // this CTA's slices, in scan order
-  float2 cta_map[2][kMaxCluster][32 * V];    // the cluster's tiles, in scan order
+  Map<V> warp[2][kWarps][32];      // this CTA's slices, in scan order
+  Map<V> cta[2][kMaxCluster][32];  // the cluster's tiles, in scan order
 };
 
 // Shares the map of this thread's slice (scan order: CTA `rank`, warp `w`) and
 // turns carry, the state before the cluster-tile, into the state before the
 // slice (returned in c) and the state behind the cluster-tile (carry).
 template <int V>
-__device__ __forceinline__ void scan_exchange(Exchange<V>& ex, int set, const float (&G)[V],
-                                              const float (&H)[V], float (&carry)[V],
-                                              float (&c)[V], int w, int W, int lane,
+__device__ __forceinline__ void scan_exchange(Exchange<V>& ex, int set, const Map<V>& mine,
+                                              float (&carry)[V], float (&c)[V], int w, int lane,
                                               unsigned rank, unsigned n) {
-#pragma unroll
-  for (int e = 0; e < V; ++e) ex.warp_map[set][w][lane * V + e] = make_float2(G[e], H[e]);
+  ex.warp[set][w][lane] = mine;
   __syncthreads();
-  if (n > 1) {
-    // warp w composes the CTA's map for the CTAs w, w + W, ...
-    if (w < n) {
-      float2 m[V];
-#pragma unroll
-      for (int e = 0; e < V; ++e) m[e] = ex.warp_map[set][0][lane * V + e];
-      for (int i = 1; i < W; ++i)
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-          const float2 y = ex.warp_map[set][i][lane * V + e];
-          m[e] = make_float2(m[e].x + y.x, apply(y, m[e].y));
-        }
-      for (unsigned r = w; r < n; r += W)
-#pragma unroll
-        for (int e = 0; e < V; ++e) store_remote(&ex.cta_map[set][rank][lane * V + e], r, m[e]);
-    }
-    cluster_barrier();
-  }
 #pragma unroll
   for (int e = 0; e < V; ++e) c[e] = carry[e];
   if (n > 1) {
-    for (unsigned r = 0; r < n; ++r)
+    if (w < n) {  // warp w composes the CTA's map for the CTAs w, w + kWarps, ...
+      Map<V> m = ex.warp[set][0][lane];
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        if (r == rank) c[e] = carry[e];
-        carry[e] = apply(ex.cta_map[set][r][lane * V + e], carry[e]);
+      for (int i = 1; i < kWarps; ++i) {
+        const Map<V> y = ex.warp[set][i][lane];
+        apply(y, m.H);
+#pragma unroll
+        for (int e = 0; e < V; ++e) m.A[e] = finite(m.A[e] * y.A[e]);
       }
-    for (int i = 0; i < w; ++i)
+      for (unsigned r = w; r < n; r += kWarps) store_remote(&ex.cta[set][rank][lane], r, m);
+    }
+    cluster_barrier();
+    for (unsigned r = 0; r < n; ++r) {
+      if (r == rank) {
 #pragma unroll
-      for (int e = 0; e < V; ++e) c[e] = apply(ex.warp_map[set][i][lane * V + e], c[e]);
+        for (int e = 0; e < V; ++e) c[e] = carry[e];
+      }
+      apply(ex.cta[set][r][lane], carry);
+    }
+#pragma unroll
+    for (int i = 0; i < kWarps - 1; ++i)
+      if (i < w) apply(ex.warp[set][i][lane], c);
   } else {
-    for (int i = 0; i < W; ++i)
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        if (i == w) c[e] = carry[e];
-        carry[e] = apply(ex.warp_map[set][i][lane * V + e], carry[e]);
+    for (int i = 0; i < kWarps; ++i) {
+      if (i == w) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) c[e] = carry[e];
       }
+      apply(ex.warp[set][i][lane], carry);
+    }
   }
 }
 
+// r[i] = the V elements at p + i stride for i < cnt, zeros behind them.  A whole
+// slice is loaded without predicates.
+template <typename T, int V, int S>
+__device__ __forceinline__ void load_slice(Vec<T, V> (&r)[S], const T* p, size_t stride, int cnt) {
+  if (cnt == S) {
+#pragma unroll
+    for (int i = 0; i < S; ++i) r[i] = load<T, V>(p + i * stride);
+  } else {
+#pragma unroll
+    for (int i = 0; i < S; ++i) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) r[i].v[e] = from_f<T>(0.f);
+      if (i < cnt) r[i] = load<T, V>(p + i * stride);
+    }
+  }
+}
+
+__device__ __forceinline__ float decay(float g) { return __expf(g); }
+
 template <typename T, int V, int S, bool BETA>
-__global__ void __launch_bounds__(32 * kMaxWarps, 2) scan_kernel(const ScanArgs a) {
+__global__ void __launch_bounds__(32 * kWarps, 4) scan_kernel(const ScanArgs a) {
   __shared__ Exchange<V> ex;
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, W = blockDim.x >> 5;
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const unsigned n = cluster_size(), rank = cluster_rank();
   const int id = blockIdx.x / n, seq = id / a.cblocks;
-  const int c0 = (id % a.cblocks) * 32 * V + lane * V;
+  int c0 = (id % a.cblocks) * 32 * V + lane * V;
   const bool on = c0 < a.C;
+  if (!on) c0 = a.C - V;  // lanes past the last channel repeat it and store nothing
   Seq s;
   if (!sequence(a, seq, &s)) {  // the same answer in every CTA of the cluster
     if (a.status && threadIdx.x == 0 && rank == 0) *a.status = GDN_ERR_SHAPE;
@@ -162,56 +191,59 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 2) scan_kernel(const ScanArgs 
   float carry[V];
 #pragma unroll
   for (int e = 0; e < V; ++e) carry[e] = 0.f;
-  if (a.h0 && on) {
+  if (a.h0) {
     const Vec<float, V> v = load<float, V>(a.h0 + (size_t)seq * a.C + c0);
 #pragma unroll
     for (int e = 0; e < V; ++e) carry[e] = v.v[e];
   }
-  const int tile = W * S, step = tile * int(n);
+  constexpr int tile = kWarps * S;
+  const int step = tile * int(n);
   int set = 0;
   for (int base = 0; base < s.len; base += step, set ^= 1) {
     const int t0 = base + int(rank) * tile + w * S;
-    const int cnt = on ? min(max(s.len - t0, 0), S) : 0;
+    const int cnt = min(max(s.len - t0, 0), S);  // the same in every lane
     const size_t at = size_t(s.start + t0) * a.C + c0;
-    const T* px = static_cast<const T*>(a.x) + at;
-    const T* pb = static_cast<const T*>(a.beta) + at;
-    const float* pg = a.g + at;
+    // tokens past the end are g = x = 0: they leave the state as it is
     Vec<float, V> g[S];
-    Vec<T, V> x[S], b[BETA ? S : 1];
+    Vec<T, V> x[S], b[S];
+    load_slice<float, V, S>(g, a.g + at, a.C, cnt);
+    load_slice<T, V, S>(x, static_cast<const T*>(a.x) + at, a.C, cnt);
+    if (BETA) load_slice<T, V, S>(b, static_cast<const T*>(a.beta) + at, a.C, cnt);
+    float al[S][V], u[S][V], h[V];
+    Map<V> m;
 #pragma unroll
-    for (int i = 0; i < S; ++i)
-      if (i < cnt) {
-        g[i] = load<float, V>(pg + (size_t)i * a.C);
-        x[i] = load<T, V>(px + (size_t)i * a.C);
-        if (BETA) b[i] = load<T, V>(pb + (size_t)i * a.C);
-      }
-    float al[S][V], u[S][V], G[V], H[V];
-#pragma unroll
-    for (int e = 0; e < V; ++e) G[e] = H[e] = 0.f;
+    for (int e = 0; e < V; ++e) m.A[e] = m.H[e] = 0.f;
 #pragma unroll
     for (int i = 0; i < S; ++i)
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        // tokens past the end (and channels past C) leave the state as it is
-        al[i][e] = i < cnt ? expf(g[i].v[e]) : 1.f;
-        u[i][e] = i < cnt ? to_f(x[i].v[e]) : 0.f;
-        if (BETA) u[i][e] *= i < cnt ? to_f(b[i].v[e]) : 0.f;
-        G[e] += i < cnt ? g[i].v[e] : 0.f;
-        H[e] = fmaf(al[i][e], H[e], u[i][e]);
+        al[i][e] = decay(g[i].v[e]);
+        u[i][e] = BETA ? to_f(x[i].v[e]) * to_f(b[i].v[e]) : to_f(x[i].v[e]);
+        m.A[e] += g[i].v[e];
+        m.H[e] = fmaf(al[i][e], m.H[e], u[i][e]);
       }
-    float h[V];
-    scan_exchange<V>(ex, set, G, H, carry, h, w, W, lane, rank, n);
-    if (cnt > 0 && a.carries && t0 % kCarryTokens == 0)
-      store<float, V>(a.carries + size_t(s.carry_row + t0 / kCarryTokens) * a.C + c0, h);
-    if (a.h) {
-      T* ph = static_cast<T*>(a.h) + at;
 #pragma unroll
-      for (int i = 0; i < S; ++i)
-        if (i < cnt) {
+    for (int e = 0; e < V; ++e) m.A[e] = finite(expf(m.A[e]));
+    scan_exchange<V>(ex, set, m, carry, h, w, lane, rank, n);
+    if (cnt > 0 && on && a.carries && t0 % kCarryTokens == 0)
+      store<float, V>(a.carries + size_t(s.carry_row + t0 / kCarryTokens) * a.C + c0, h);
+    if (a.h && on) {
+      T* ph = static_cast<T*>(a.h) + at;
+      if (cnt == S) {
+#pragma unroll
+        for (int i = 0; i < S; ++i) {
 #pragma unroll
           for (int e = 0; e < V; ++e) h[e] = fmaf(al[i][e], h[e], u[i][e]);
           store<T, V>(ph + (size_t)i * a.C, h);
         }
+      } else {
+#pragma unroll
+        for (int i = 0; i < S; ++i) {
+#pragma unroll
+          for (int e = 0; e < V; ++e) h[e] = fmaf(al[i][e], h[e], u[i][e]);
+          if (i < cnt) store<T, V>(ph + (size_t)i * a.C, h);
+        }
+      }
     }
   }
   if (a.h_T && rank == 0 && w == 0 && on)
@@ -223,17 +255,18 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 2) scan_kernel(const ScanArgs 
 // states that the forward pass kept every 16 tokens: reading them costs 4/16
 // byte an element, reading h itself 2 to 4 and, in bf16, its rounding in dg.
 template <typename T, int V, int S, bool BETA>
-__global__ void __launch_bounds__(32 * kMaxWarps, 2) scan_backward_kernel(const ScanBackwardArgs a) {
+__global__ void __launch_bounds__(32 * kWarps, 4) scan_backward_kernel(const ScanBackwardArgs a) {
   __shared__ Exchange<V> ex;
-  // the odd slices of a kept state's 16 tokens start from the slices before
+  // the later slices of a kept state's 16 tokens start from the slices before
   constexpr int M = kCarryTokens / S;
-  __shared__ float2 fwd_map[M > 1 ? 2 : 1][M > 1 ? kMaxWarps : 1][32 * V];
+  __shared__ Map<V> fwd[M > 1 ? 2 : 1][M > 1 ? kWarps : 1][32];
   const ScanArgs& f = a.f;
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, W = blockDim.x >> 5;
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const unsigned n = cluster_size(), rank = cluster_rank();
   const int id = blockIdx.x / n, seq = id / f.cblocks;
-  const int c0 = (id % f.cblocks) * 32 * V + lane * V;
+  int c0 = (id % f.cblocks) * 32 * V + lane * V;
   const bool on = c0 < f.C;
+  if (!on) c0 = f.C - V;
   Seq s;
   if (!sequence(f, seq, &s)) {
     if (f.status && threadIdx.x == 0 && rank == 0) *f.status = GDN_ERR_SHAPE;
@@ -243,90 +276,88 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 2) scan_backward_kernel(const 
   float carry[V];
 #pragma unroll
   for (int e = 0; e < V; ++e) carry[e] = 0.f;
-  if (a.dh_T && on) {
+  if (a.dh_T) {
     const Vec<float, V> v = load<float, V>(a.dh_T + (size_t)seq * f.C + c0);
 #pragma unroll
     for (int e = 0; e < V; ++e) carry[e] = v.v[e];
   }
-  const int tile = W * S, tiles = (s.len + tile - 1) / tile;
+  constexpr int tile = kWarps * S;
+  const int tiles = (s.len + tile - 1) / tile;
+  const int sw = kWarps - 1 - w;  // scan order runs backwards in time
   int set = 0;
   for (int first = 0; first < tiles; first += int(n), set ^= 1) {
-    // scan order runs backwards in time; a tile index below 0 is past the start
-    const int ti = tiles - 1 - first - int(rank);
-    const int sw = W - 1 - w;  // the slice of this warp within the tile
+    const int ti = tiles - 1 - first - int(rank);  // below 0: past the start
     const int t0 = ti * tile + sw * S;
-    const int cnt = on && ti >= 0 ? min(max(s.len - t0, 0), S) : 0;
+    const int cnt = ti >= 0 ? min(max(s.len - t0, 0), S) : 0;
     const size_t at = cnt > 0 ? size_t(s.start + t0) * f.C + c0 : 0;
     Vec<float, V> g[S], hc;
-    Vec<T, V> x[S], b[BETA ? S : 1], d[S];
+    Vec<T, V> x[S], b[S], d[S];
+    load_slice<float, V, S>(g, f.g + at, f.C, cnt);
+    load_slice<T, V, S>(d, static_cast<const T*>(a.dh) + at, f.C, cnt);
+    load_slice<T, V, S>(x, static_cast<const T*>(f.x) + at, f.C, cnt);
+    if (BETA) load_slice<T, V, S>(b, static_cast<const T*>(f.beta) + at, f.C, cnt);
 #pragma unroll
-    for (int i = 0; i < S; ++i)
-      if (i < cnt) {
-        const size_t o = at + (size_t)i * f.C;
-        g[i] = load<float, V>(f.g + o);
-        d[i] = load<T, V>(static_cast<const T*>(a.dh) + o);
-        x[i] = load<T, V>(static_cast<const T*>(f.x) + o);
-        if (BETA) b[i] = load<T, V>(static_cast<const T*>(f.beta) + o);
-      }
+    for (int e = 0; e < V; ++e) hc.v[e] = 0.f;
     if (cnt > 0)
       hc = load<float, V>(f.carries + size_t(s.carry_row + t0 / kCarryTokens) * f.C + c0);
-    float al[S][V], G[V], R[V], H[V];
+    float al[S][V];
+    Map<V> m, mf;
 #pragma unroll
-    for (int e = 0; e < V; ++e) G[e] = R[e] = H[e] = 0.f;
+    for (int e = 0; e < V; ++e) m.A[e] = m.H[e] = mf.H[e] = 0.f;
 #pragma unroll
     for (int i = 0; i < S; ++i)
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        al[i][e] = i < cnt ? expf(g[i].v[e]) : 1.f;
-        G[e] += i < cnt ? g[i].v[e] : 0.f;
-        if (M > 1 && i < cnt) {
+        al[i][e] = decay(g[i].v[e]);
+        m.A[e] += g[i].v[e];
+        if (M > 1) {
           const float u = BETA ? to_f(x[i].v[e]) * to_f(b[i].v[e]) : to_f(x[i].v[e]);
-          H[e] = fmaf(al[i][e], H[e], u);
+          mf.H[e] = fmaf(al[i][e], mf.H[e], u);
         }
       }
 #pragma unroll
     for (int i = S - 1; i >= 0; --i)
 #pragma unroll
-      for (int e = 0; e < V; ++e)
-        if (i < cnt) R[e] = al[i][e] * (to_f(d[i].v[e]) + R[e]);
+      for (int e = 0; e < V; ++e) m.H[e] = al[i][e] * (to_f(d[i].v[e]) + m.H[e]);
+#pragma unroll
+    for (int e = 0; e < V; ++e) mf.A[e] = m.A[e] = finite(expf(m.A[e]));
+    if (M > 1) fwd[set][sw][lane] = mf;
+    float mu[V];
+    scan_exchange<V>(ex, set, m, carry, mu, w, lane, rank, n);
+    float hp[S][V];  // h before each token
+    float h[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) h[e] = hc.v[e];
     if (M > 1) {
 #pragma unroll
-      for (int e = 0; e < V; ++e) fwd_map[set][sw][lane * V + e] = make_float2(G[e], H[e]);
+      for (int i = 0; i < M - 1; ++i)
+        if (i < sw % M) apply(fwd[set][sw - sw % M + i][lane], h);
     }
-    float mu[V];
-    scan_exchange<V>(ex, set, G, R, carry, mu, w, W, lane, rank, n);
-    float hp[S][V];  // h before each token
-    if (cnt > 0) {
+#pragma unroll
+    for (int i = 0; i < S; ++i)
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        float h = hc.v[e];
-        if (M > 1)
-          for (int i = sw - sw % M; i < sw; ++i) h = apply(fwd_map[set][i][lane * V + e], h);
-#pragma unroll
-        for (int i = 0; i < S; ++i)
-          if (i < cnt) {
-            hp[i][e] = h;
-            const float u = BETA ? to_f(x[i].v[e]) * to_f(b[i].v[e]) : to_f(x[i].v[e]);
-            h = fmaf(al[i][e], h, u);
-          }
+        hp[i][e] = h[e];
+        const float u = BETA ? to_f(x[i].v[e]) * to_f(b[i].v[e]) : to_f(x[i].v[e]);
+        h[e] = fmaf(al[i][e], h[e], u);
       }
 #pragma unroll
-      for (int i = S - 1; i >= 0; --i)
-        if (i < cnt) {
-          float dx[V], db[V], dg[V];
+    for (int i = S - 1; i >= 0; --i) {
+      float dx[V], db[V], dg[V];
 #pragma unroll
-          for (int e = 0; e < V; ++e) {
-            const float lam = to_f(d[i].v[e]) + mu[e];
-            mu[e] = al[i][e] * lam;
-            dg[e] = mu[e] * hp[i][e];
-            dx[e] = BETA ? lam * to_f(b[i].v[e]) : lam;
-            db[e] = lam * to_f(x[i].v[e]);
-          }
-          const size_t o = at + (size_t)i * f.C;
-          store<T, V>(static_cast<T*>(a.dx) + o, dx);
-          store<float, V>(a.dg + o, dg);
-          if (BETA) store<T, V>(static_cast<T*>(a.dbeta) + o, db);
-        }
+      for (int e = 0; e < V; ++e) {
+        const float lam = to_f(d[i].v[e]) + mu[e];
+        mu[e] = al[i][e] * lam;
+        dg[e] = mu[e] * hp[i][e];
+        dx[e] = BETA ? lam * to_f(b[i].v[e]) : lam;
+        db[e] = lam * to_f(x[i].v[e]);
+      }
+      if (on && i < cnt) {
+        const size_t o = at + (size_t)i * f.C;
+        store<T, V>(static_cast<T*>(a.dx) + o, dx);
+        store<float, V>(a.dg + o, dg);
+        if (BETA) store<T, V>(static_cast<T*>(a.dbeta) + o, db);
+      }
     }
   }
   if (a.dh0 && rank == 0 && w == 0 && on)
@@ -353,35 +384,28 @@ __global__ void __launch_bounds__(256) scan_step_kernel(const T* x, const float*
   store<T, V>(h + i, r);
 }
 
-struct Shape {
-  int warps, cluster;
-};
-
-// Warps: enough for the sequence, at most 8.  Cluster: the fewest CTAs along
-// time that give every SM two CTAs, as long as each has tokens.
-Shape pick_shape(const ScanArgs& a, int S, int min_warps, long long chains, int sms) {
-  const long long avg = a.cu_seqlens ? std::max<long long>(1, a.T / std::max(1, a.N)) : a.T;
-  const long long slices = (avg + S - 1) / S;
-  int W = min_warps;
-  while (W < kMaxWarps && W < slices) W *= 2;
+// CTAs along time: the fewest that give every SM four, as long as each has
+// tokens of a sequence of average length.
+int pick_cluster(const ScanArgs& a, int S, long long chains, int sms) {
+  const long long len = a.cu_seqlens ? std::max<long long>(1, a.T / std::max(1, a.N)) : a.T;
   int n = 1;
-  while (n < kMaxCluster && chains * n < 2LL * sms && (long long)n * W < slices) n *= 2;
-  return {W, n};
+  while (n < kMaxCluster && chains * n < 4LL * sms && (long long)n * kWarps * S < len) n *= 2;
+  return n;
 }
 
 template <typename Args>
-bool launch_cluster(void (*kernel)(const Args), const Args& args, long long ctas, Shape sh,
+bool launch_cluster(void (*kernel)(const Args), const Args& args, long long ctas, int n,
                     cudaStream_t stream) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(unsigned(ctas * sh.cluster));
-  cfg.blockDim = dim3(unsigned(32 * sh.warps));
+  cfg.gridDim = dim3(unsigned(ctas * n));
+  cfg.blockDim = dim3(32 * kWarps);
   cfg.stream = stream;
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim.x = unsigned(sh.cluster);
+  at.val.clusterDim.x = unsigned(n);
   at.val.clusterDim.y = at.val.clusterDim.z = 1;
   cfg.attrs = &at;
-  cfg.numAttrs = sh.cluster > 1 ? 1 : 0;
+  cfg.numAttrs = n > 1 ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kernel, args) == cudaSuccess;
 }
 
@@ -390,21 +414,22 @@ int run_scan(ScanArgs a, int sms, cudaStream_t stream) {
   a.cblocks = (a.C + 32 * V - 1) / (32 * V);
   const long long chains = (long long)a.cblocks * a.N;
   if (chains * kMaxCluster > 0x7fffffffLL) return GDN_ERR_SHAPE;
-  const Shape sh = pick_shape(a, S, 1, chains, sms);
-  const bool ok = a.beta ? launch_cluster(&scan_kernel<T, V, S, true>, a, chains, sh, stream)
-                         : launch_cluster(&scan_kernel<T, V, S, false>, a, chains, sh, stream);
+  const int n = pick_cluster(a, S, chains, sms);
+  const bool ok = a.beta ? launch_cluster(&scan_kernel<T, V, S, true>, a, chains, n, stream)
+                         : launch_cluster(&scan_kernel<T, V, S, false>, a, chains, n, stream);
   return ok ? GDN_OK : GDN_ERR_LAUNCH;
 }
 
 template <typename T, int V, int S>
 int run_backward(ScanBackwardArgs a, int sms, cudaStream_t stream) {
+  static_assert(kWarps * S % kCarryTokens == 0, "a tile starts at a kept state");
   a.f.cblocks = (a.f.C + 32 * V - 1) / (32 * V);
   const long long chains = (long long)a.f.cblocks * a.f.N;
   if (chains * kMaxCluster > 0x7fffffffLL) return GDN_ERR_SHAPE;
-  const Shape sh = pick_shape(a.f, S, kCarryTokens / S, chains, sms);
+  const int n = pick_cluster(a.f, S, chains, sms);
   const bool ok =
-      a.f.beta ? launch_cluster(&scan_backward_kernel<T, V, S, true>, a, chains, sh, stream)
-               : launch_cluster(&scan_backward_kernel<T, V, S, false>, a, chains, sh, stream);
+      a.f.beta ? launch_cluster(&scan_backward_kernel<T, V, S, true>, a, chains, n, stream)
+               : launch_cluster(&scan_backward_kernel<T, V, S, false>, a, chains, n, stream);
   return ok ? GDN_OK : GDN_ERR_LAUNCH;
 }
 

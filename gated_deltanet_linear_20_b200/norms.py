@@ -84,8 +84,8 @@ def gated_norm(x: torch.Tensor, w: torch.Tensor, z: Optional[torch.Tensor] = Non
     px = _expect(x, "x", x.dtype, shape, dev)
     pw = _expect(w, "w", _F32, (D,), dev)
     pz = _optional(z, "z", out_dtype, shape, dev)
-    y = _out(y, "y", out_dtype, shape, dev)
-    _call("gdn_gated_norm", dev, px, xt, pw, pz, y.data_ptr(), rows, D, _dtype(y, "y"),
+    y = _out(y, "y", out_dtype, shape, dev, x)
+    _call(_lib.gdn_gated_norm, dev, px, xt, pw, pz, y.data_ptr(), rows, D, _dtype(y, "y"),
           _options(eps, weight_offset, gate))
     return y
 
@@ -109,7 +109,7 @@ def gated_norm_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor,
     dz = torch.empty_like(z) if z is not None else None
     dw = torch.empty_like(w)
     ws, have = _workspace(workspace, rows, D, 1, dev)
-    _call("gdn_gated_norm_backward", dev, pdy, px, xt, pw, pz, dx.data_ptr(),
+    _call(_lib.gdn_gated_norm_backward, dev, pdy, px, xt, pw, pz, dx.data_ptr(),
           None if dz is None else dz.data_ptr(), dw.data_ptr(), rows, D, dt, ws.data_ptr(), have,
           _options(eps, weight_offset, gate))
     return dx, dz, dw
@@ -139,9 +139,9 @@ def residual_norm(x: torch.Tensor, r: torch.Tensor, w: torch.Tensor, *,
     pz = _optional(z, "z", x.dtype, shape, dev)
     pp = _optional(w_post, "w_post", _F32, (D,), dev)
     ps = _optional(scale, "scale", _F32, (D,), dev)
-    y = _out(y, "y", x.dtype, shape, dev)
-    r_out = _out(r_out, "r_out", r.dtype, shape, dev)
-    _call("gdn_residual_norm", dev, px, pr, pw, pz, pp, ps, y.data_ptr(), r_out.data_ptr(), rows,
+    y = _out(y, "y", x.dtype, shape, dev, x)
+    r_out = _out(r_out, "r_out", r.dtype, shape, dev, r)
+    _call(_lib.gdn_residual_norm, dev, px, pr, pw, pz, pp, ps, y.data_ptr(), r_out.data_ptr(), rows,
           D, dt, rt, _options(eps, weight_offset, gate))
     return y, r_out
 
@@ -175,7 +175,7 @@ def residual_norm_backward(dy: torch.Tensor, dr_out: Optional[torch.Tensor], x: 
     dsc = torch.empty_like(scale) if scale is not None else None
     ws, have = _workspace(workspace, rows, D, 1 + (dwp is not None) + (dsc is not None), dev)
     at = lambda t: None if t is None else t.data_ptr()  # noqa: E731
-    _call("gdn_residual_norm_backward", dev, pdy, pdr, px, pr, pw, pz, pp, ps, dx.data_ptr(),
+    _call(_lib.gdn_residual_norm_backward, dev, pdy, pdr, px, pr, pw, pz, pp, ps, dx.data_ptr(),
           dr.data_ptr(), at(dz), dw.data_ptr(), at(dwp), at(dsc), rows, D, dt, rt, ws.data_ptr(),
           have, _options(eps, weight_offset, gate))
     return dx, dr, dz, dw, dwp, dsc

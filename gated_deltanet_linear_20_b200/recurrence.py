@@ -60,25 +60,29 @@ def _dtype(t: torch.Tensor, name: str) -> int:
     return code
 
 
-def _call(name: str, device: torch.device, *args):
-    """Calls the library on the tensors' device and its current stream."""
-    fn = getattr(_lib, name)
-    stream = torch.cuda.current_stream(device).cuda_stream
-    if torch.cuda.current_device() == device.index:
+def _call(fn, device: torch.device, *args):
+    """Calls the library on the tensors' device and that device's current stream.
+    (The stream's handle is asked for directly: torch.cuda.current_stream builds
+    an object first, 2.2 us against 0.1 of a call that takes 8 in all.)"""
+    index = device.index
+    stream = torch._C._cuda_getCurrentRawStream(index)
+    if torch._C._cuda_getDevice() == index:
         rc = fn(*args, stream)
     else:
         with torch.cuda.device(device):
             rc = fn(*args, stream)
     if rc != GDN_OK:
-        raise GDNError(rc, name)
+        raise GDNError(rc, fn.__name__)
 
 
-def _out(t, name, dtype, shape, device):
-    """A given output, checked, or a new one."""
+def _out(t, name, dtype, shape, device, like=None):
+    """A given output, checked, or a new one (``like``: a tensor of its shape, which
+    is quicker to copy the shape from)."""
     if t is None:
-        t = torch.empty(shape, dtype=dtype, device=device)
-    else:
-        _check(t, name, dtype, shape, device)
+        if like is not None:
+            return torch.empty_like(like) if like.dtype is dtype else torch.empty_like(like, dtype=dtype)
+        return torch.empty(shape, dtype=dtype, device=device)
+    _check(t, name, dtype, shape, device)
     return t
 
 
@@ -108,11 +112,11 @@ def scan(x: torch.Tensor, g: torch.Tensor, beta: Optional[torch.Tensor] = None,
     pg = _expect(g, "g", _F32, shape, dev)
     pb = _optional(beta, "beta", x.dtype, shape, dev)
     p0 = _optional(h0, "h0", _F32, (B, C), dev)
-    h = _out(h, "h", x.dtype, shape, dev)
+    h = _out(h, "h", x.dtype, shape, dev, x)
     h_T = _out(h_T, "h_T", _F32, (B, C), dev)
     carries = torch.empty(_carry_shape(B, B * T, C, False), dtype=_F32, device=dev) \
         if save_carries else None
-    _call("gdn_scan", dev, px, pg, pb, p0, h.data_ptr(), h_T.data_ptr(),
+    _call(_lib.gdn_scan, dev, px, pg, pb, p0, h.data_ptr(), h_T.data_ptr(),
           None if carries is None else carries.data_ptr(), B, T, C, dt)
     return (h, h_T, carries) if save_carries else (h, h_T)
 
@@ -143,11 +147,11 @@ def scan_varlen(x: torch.Tensor, g: torch.Tensor, cu_seqlens: torch.Tensor,
     pg = _expect(g, "g", _F32, shape, dev)
     pb = _optional(beta, "beta", x.dtype, shape, dev)
     p0 = _optional(h0, "h0", _F32, (N, C), dev)
-    h = _out(h, "h", x.dtype, shape, dev)
+    h = _out(h, "h", x.dtype, shape, dev, x)
     h_T = _out(h_T, "h_T", _F32, (N, C), dev)
     carries = torch.empty(_carry_shape(N, T, C, True), dtype=_F32, device=dev) \
         if save_carries else None
-    _call("gdn_scan_varlen", dev, px, pg, pb, p0, h.data_ptr(), h_T.data_ptr(),
+    _call(_lib.gdn_scan_varlen, dev, px, pg, pb, p0, h.data_ptr(), h_T.data_ptr(),
           None if carries is None else carries.data_ptr(), pcu, N, T, C, dt, pst)
     return (h, h_T, carries) if save_carries else (h, h_T)
 
@@ -169,12 +173,12 @@ def scan_step(x: torch.Tensor, g: torch.Tensor, state: torch.Tensor,
     pg = _expect(g, "g", _F32, shape, dev)
     ps = _expect(state, "state", _F32, shape, dev)
     pb = _optional(beta, "beta", x.dtype, shape, dev)
-    h = _out(h, "h", x.dtype, shape, dev)
-    _call("gdn_scan_step", dev, px, pg, pb, ps, h.data_ptr(), B, C, dt)
+    h = _out(h, "h", x.dtype, shape, dev, x)
+    _call(_lib.gdn_scan_step, dev, px, pg, pb, ps, h.data_ptr(), B, C, dt)
     return h
 
 
-def _backward(name, dh, x, g, beta, h0, dh_T, carries, N, tokens, packed, sizes,
+def _backward(fn, dh, x, g, beta, h0, dh_T, carries, N, tokens, packed, sizes,
               tail, dev):
     shape, C = x.shape, x.shape[-1]
     dt = _dtype(x, "x")
@@ -190,7 +194,7 @@ def _backward(name, dh, x, g, beta, h0, dh_T, carries, N, tokens, packed, sizes,
     dg = torch.empty_like(g)
     dbeta = torch.empty_like(beta) if beta is not None else None
     dh0 = torch.empty_like(h0) if h0 is not None else None
-    _call(name, dev, px, pg, pb, p0, pdh, pdt, dx.data_ptr(), dg.data_ptr(),
+    _call(fn, dev, px, pg, pb, p0, pdh, pdt, dx.data_ptr(), dg.data_ptr(),
           None if dbeta is None else dbeta.data_ptr(), None if dh0 is None else dh0.data_ptr(),
           carries.data_ptr(), int(kept), *sizes, C, dt, *tail)
     return dx, dg, dbeta, dh0
@@ -209,7 +213,7 @@ def scan_backward(dh: torch.Tensor, x: torch.Tensor, g: torch.Tensor,
     if x.dim() != 3:
         raise ValueError("x must be [B,T,C]")
     B, T, _ = x.shape
-    return _backward("gdn_scan_backward", dh, x, g, beta, h0, dh_T, carries, B, B * T, False,
+    return _backward(_lib.gdn_scan_backward, dh, x, g, beta, h0, dh_T, carries, B, B * T, False,
                      (B, T), (), dev)
 
 
@@ -223,5 +227,5 @@ def scan_varlen_backward(dh: torch.Tensor, x: torch.Tensor, g: torch.Tensor,
     dev = _device(x, "scan_varlen_backward")
     N, pcu, pst = _packed(x, cu_seqlens, status, dev)
     T = x.shape[0]
-    return _backward("gdn_scan_varlen_backward", dh, x, g, beta, h0, dh_T, carries, N, T, True,
+    return _backward(_lib.gdn_scan_varlen_backward, dh, x, g, beta, h0, dh_T, carries, N, T, True,
                      (pcu, N, T), (pst,), dev)
