@@ -349,9 +349,9 @@ int static_workspace(void** out) {
 
 namespace gdn {
 bool ensure_smem_attr(const void* func, int slot, int bytes) {
-  static std::atomic<uint64_t> done[96];  // bit d: device d, per kernel slot
+  static std::atomic<uint64_t> done[128];  // bit d: device d, per kernel slot
   int dev = 0;
-  if (slot < 0 || slot >= 96 || cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64)
+  if (slot < 0 || slot >= 128 || cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64)
     return false;
   const uint64_t bit = uint64_t(1) << dev;
   if (done[slot].load(std::memory_order_acquire) & bit) return true;

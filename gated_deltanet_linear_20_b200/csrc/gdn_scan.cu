@@ -25,6 +25,7 @@
 // hardware barriers, and the order of every sum is fixed: results do not
 // depend on timing.
 #include <algorithm>
+#include <type_traits>
 
 #include "gdn_internal.h"
 #include "gdn_vec.cuh"
@@ -35,6 +36,7 @@ namespace {
 constexpr int kCarryTokens = GDN_SCAN_CARRY_TOKENS;
 constexpr int kWarps = 4;       // of a CTA, along time
 constexpr int kMaxCluster = 8;  // CTAs along time
+constexpr int kScanSlot = 96;   // ensure_smem_attr: 16 kernels
 
 // The map of a run of tokens for V channels: c -> A c + H.  A stays finite, so
 // that a state of zero stays out of a run whose growth passes the fp32 range.
@@ -154,19 +156,58 @@ __device__ __forceinline__ void scan_exchange(Exchange<V>& ex, int set, const Ma
   }
 }
 
-// r[i] = the V elements at p + i stride for i < cnt, zeros behind them.  A whole
-// slice is loaded without predicates.
-template <typename T, int V, int S>
-__device__ __forceinline__ void load_slice(Vec<T, V> (&r)[S], const T* p, size_t stride, int cnt) {
+// A thread's slice on its way from memory: the log decays and K arrays of T, copied
+// asynchronously into a place of the thread's own while it works on the slice
+// before, so no barrier is needed and no register waits for memory.  Copies
+// move at least 4 bytes: a single bf16 (V = 1) is loaded directly instead.
+template <typename T, int V, int S, int K>
+struct Stage {
+  Vec<float, V> g[S][32 * kWarps];
+  Vec<T, V> t[K][S][32 * kWarps];
+};
+template <typename T, int V>
+constexpr bool kAsync = sizeof(T) * V >= 4;
+
+template <typename E>
+__device__ __forceinline__ void copy_async(E* dst, const E* src, int bytes) {
+  const unsigned d = static_cast<unsigned>(__cvta_generic_to_shared(dst));
+  // bytes behind `bytes` (0 or all) are zeros
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(d), "l"(src),
+               "n"(sizeof(E)), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// Starts the copies of tokens 0 .. cnt - 1 of a slice at p; zeros behind them.
+template <typename E, int S>
+__device__ __forceinline__ void fetch(E (&dst)[S][32 * kWarps], const void* p, size_t stride,
+                                      int cnt) {
+  const char* q = static_cast<const char*>(p);
   if (cnt == S) {
 #pragma unroll
-    for (int i = 0; i < S; ++i) r[i] = load<T, V>(p + i * stride);
+    for (int i = 0; i < S; ++i)
+      copy_async(&dst[i][threadIdx.x], reinterpret_cast<const E*>(q + i * stride), sizeof(E));
   } else {
 #pragma unroll
-    for (int i = 0; i < S; ++i) {
+    for (int i = 0; i < S; ++i)
+      copy_async(&dst[i][threadIdx.x], reinterpret_cast<const E*>(i < cnt ? q + i * stride : q),
+                 i < cnt ? sizeof(E) : 0);
+  }
+}
+
+// The slice's elements in registers: from the stage, or (async false) from memory.
+template <bool ASYNC, typename E, int S>
+__device__ __forceinline__ void take(E (&r)[S], const E (&src)[S][32 * kWarps], const void* p,
+                                     size_t stride, int cnt) {
+  if constexpr (ASYNC) {
 #pragma unroll
-      for (int e = 0; e < V; ++e) r[i].v[e] = from_f<T>(0.f);
-      if (i < cnt) r[i] = load<T, V>(p + i * stride);
+    for (int i = 0; i < S; ++i) r[i] = src[i][threadIdx.x];
+  } else {
+    const char* q = static_cast<const char*>(p);
+#pragma unroll
+    for (int i = 0; i < S; ++i) {
+      r[i] = E{};
+      if (i < cnt) r[i] = *reinterpret_cast<const E*>(q + i * stride);
     }
   }
 }
@@ -175,7 +216,10 @@ __device__ __forceinline__ float decay(float g) { return __expf(g); }
 
 template <typename T, int V, int S, bool BETA>
 __global__ void __launch_bounds__(32 * kWarps, 4) scan_kernel(const ScanArgs a) {
-  __shared__ Exchange<V> ex;
+  constexpr bool kStaged = kAsync<T, V>;
+  extern __shared__ __align__(16) unsigned char smem[];
+  auto& ex = *reinterpret_cast<Exchange<V>*>(smem);
+  auto& st = *reinterpret_cast<Stage<T, V, S, BETA ? 2 : 1>*>(smem + sizeof(Exchange<V>));
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const unsigned n = cluster_size(), rank = cluster_rank();
   const int id = blockIdx.x / n, seq = id / a.cblocks;
@@ -198,17 +242,32 @@ __global__ void __launch_bounds__(32 * kWarps, 4) scan_kernel(const ScanArgs a) 
   }
   constexpr int tile = kWarps * S;
   const int step = tile * int(n);
+  const size_t gs = size_t(a.C) * 4, ts = size_t(a.C) * sizeof(T);
+  int t0 = int(rank) * tile + w * S, cnt = 0;
+  const char *pg = nullptr, *px = nullptr, *pb = nullptr;  // this thread's slice
+  // the slice at token t0: tokens past the end are g = x = 0, which leaves the
+  // state as it is; cnt is the same in every lane
+  const auto place = [&] {
+    cnt = min(max(s.len - t0, 0), S);
+    const size_t at = cnt > 0 ? size_t(s.start + t0) * a.C + c0 : 0;
+    pg = reinterpret_cast<const char*>(a.g + at);
+    px = reinterpret_cast<const char*>(static_cast<const T*>(a.x) + at);
+    if (BETA) pb = reinterpret_cast<const char*>(static_cast<const T*>(a.beta) + at);
+    if constexpr (kStaged) {
+      fetch(st.g, pg, gs, cnt);
+      fetch(st.t[0], px, ts, cnt);
+      if constexpr (BETA) fetch(st.t[1], pb, ts, cnt);
+    }
+  };
+  if (s.len > 0) place();
   int set = 0;
   for (int base = 0; base < s.len; base += step, set ^= 1) {
-    const int t0 = base + int(rank) * tile + w * S;
-    const int cnt = min(max(s.len - t0, 0), S);  // the same in every lane
-    const size_t at = size_t(s.start + t0) * a.C + c0;
-    // tokens past the end are g = x = 0: they leave the state as it is
+    if (kStaged) copies_done();
     Vec<float, V> g[S];
     Vec<T, V> x[S], b[S];
-    load_slice<float, V, S>(g, a.g + at, a.C, cnt);
-    load_slice<T, V, S>(x, static_cast<const T*>(a.x) + at, a.C, cnt);
-    if (BETA) load_slice<T, V, S>(b, static_cast<const T*>(a.beta) + at, a.C, cnt);
+    take<kStaged>(g, st.g, pg, gs, cnt);
+    take<kStaged>(x, st.t[0], px, ts, cnt);
+    if (BETA) take<kStaged>(b, st.t[BETA ? 1 : 0], pb, ts, cnt);
     float al[S][V], u[S][V], h[V];
     Map<V> m;
 #pragma unroll
@@ -224,12 +283,15 @@ __global__ void __launch_bounds__(32 * kWarps, 4) scan_kernel(const ScanArgs a) 
       }
 #pragma unroll
     for (int e = 0; e < V; ++e) m.A[e] = finite(expf(m.A[e]));
+    const int now = t0, have = cnt;
+    t0 += step;
+    if (base + step < s.len) place();  // in flight through the exchange and the stores
     scan_exchange<V>(ex, set, m, carry, h, w, lane, rank, n);
-    if (cnt > 0 && on && a.carries && t0 % kCarryTokens == 0)
-      store<float, V>(a.carries + size_t(s.carry_row + t0 / kCarryTokens) * a.C + c0, h);
+    if (have > 0 && on && a.carries && now % kCarryTokens == 0)
+      store<float, V>(a.carries + size_t(s.carry_row + now / kCarryTokens) * a.C + c0, h);
     if (a.h && on) {
-      T* ph = static_cast<T*>(a.h) + at;
-      if (cnt == S) {
+      T* ph = static_cast<T*>(a.h) + (have > 0 ? size_t(s.start + now) * a.C + c0 : 0);
+      if (have == S) {
 #pragma unroll
         for (int i = 0; i < S; ++i) {
 #pragma unroll
@@ -241,7 +303,7 @@ __global__ void __launch_bounds__(32 * kWarps, 4) scan_kernel(const ScanArgs a) 
         for (int i = 0; i < S; ++i) {
 #pragma unroll
           for (int e = 0; e < V; ++e) h[e] = fmaf(al[i][e], h[e], u[i][e]);
-          if (i < cnt) store<T, V>(ph + (size_t)i * a.C, h);
+          if (i < have) store<T, V>(ph + (size_t)i * a.C, h);
         }
       }
     }
@@ -256,10 +318,14 @@ __global__ void __launch_bounds__(32 * kWarps, 4) scan_kernel(const ScanArgs a) 
 // byte an element, reading h itself 2 to 4 and, in bf16, its rounding in dg.
 template <typename T, int V, int S, bool BETA>
 __global__ void __launch_bounds__(32 * kWarps, 4) scan_backward_kernel(const ScanBackwardArgs a) {
-  __shared__ Exchange<V> ex;
+  constexpr bool kStaged = kAsync<T, V>;
   // the later slices of a kept state's 16 tokens start from the slices before
   constexpr int M = kCarryTokens / S;
-  __shared__ Map<V> fwd[M > 1 ? 2 : 1][M > 1 ? kWarps : 1][32];
+  extern __shared__ __align__(16) unsigned char smem[];
+  auto& ex = *reinterpret_cast<Exchange<V>*>(smem);
+  auto& fwd = *reinterpret_cast<Map<V>(*)[2][kWarps][32]>(smem + sizeof(Exchange<V>));
+  auto& st = *reinterpret_cast<Stage<T, V, S, BETA ? 3 : 2>*>(smem + sizeof(Exchange<V>) +
+                                                              sizeof(fwd));
   const ScanArgs& f = a.f;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const unsigned n = cluster_size(), rank = cluster_rank();
@@ -284,22 +350,38 @@ __global__ void __launch_bounds__(32 * kWarps, 4) scan_backward_kernel(const Sca
   constexpr int tile = kWarps * S;
   const int tiles = (s.len + tile - 1) / tile;
   const int sw = kWarps - 1 - w;  // scan order runs backwards in time
+  const size_t gs = size_t(f.C) * 4, ts = size_t(f.C) * sizeof(T);
+  int ti = tiles - 1 - int(rank), cnt = 0;  // the tile; below 0: past the start
+  const char *pg = nullptr, *pd = nullptr, *px = nullptr, *pb = nullptr;
+  size_t at = 0;
+  Vec<float, V> kept{};
+  const auto place = [&] {
+    const int t0 = ti * tile + sw * S;
+    cnt = ti >= 0 ? min(max(s.len - t0, 0), S) : 0;
+    at = cnt > 0 ? size_t(s.start + t0) * f.C + c0 : 0;
+    pg = reinterpret_cast<const char*>(f.g + at);
+    pd = reinterpret_cast<const char*>(static_cast<const T*>(a.dh) + at);
+    px = reinterpret_cast<const char*>(static_cast<const T*>(f.x) + at);
+    if (BETA) pb = reinterpret_cast<const char*>(static_cast<const T*>(f.beta) + at);
+    if constexpr (kStaged) {
+      fetch(st.g, pg, gs, cnt);
+      fetch(st.t[0], pd, ts, cnt);
+      fetch(st.t[1], px, ts, cnt);
+      if constexpr (BETA) fetch(st.t[2], pb, ts, cnt);
+    }
+    if (cnt > 0)
+      kept = load<float, V>(f.carries + size_t(s.carry_row + t0 / kCarryTokens) * f.C + c0);
+  };
+  if (tiles > 0) place();
   int set = 0;
   for (int first = 0; first < tiles; first += int(n), set ^= 1) {
-    const int ti = tiles - 1 - first - int(rank);  // below 0: past the start
-    const int t0 = ti * tile + sw * S;
-    const int cnt = ti >= 0 ? min(max(s.len - t0, 0), S) : 0;
-    const size_t at = cnt > 0 ? size_t(s.start + t0) * f.C + c0 : 0;
-    Vec<float, V> g[S], hc;
+    if (kStaged) copies_done();
+    Vec<float, V> g[S];
     Vec<T, V> x[S], b[S], d[S];
-    load_slice<float, V, S>(g, f.g + at, f.C, cnt);
-    load_slice<T, V, S>(d, static_cast<const T*>(a.dh) + at, f.C, cnt);
-    load_slice<T, V, S>(x, static_cast<const T*>(f.x) + at, f.C, cnt);
-    if (BETA) load_slice<T, V, S>(b, static_cast<const T*>(f.beta) + at, f.C, cnt);
-#pragma unroll
-    for (int e = 0; e < V; ++e) hc.v[e] = 0.f;
-    if (cnt > 0)
-      hc = load<float, V>(f.carries + size_t(s.carry_row + t0 / kCarryTokens) * f.C + c0);
+    take<kStaged>(g, st.g, pg, gs, cnt);
+    take<kStaged>(d, st.t[0], pd, ts, cnt);
+    take<kStaged>(x, st.t[1], px, ts, cnt);
+    if (BETA) take<kStaged>(b, st.t[BETA ? 2 : 0], pb, ts, cnt);
     float al[S][V];
     Map<V> m, mf;
 #pragma unroll
@@ -322,12 +404,15 @@ __global__ void __launch_bounds__(32 * kWarps, 4) scan_backward_kernel(const Sca
 #pragma unroll
     for (int e = 0; e < V; ++e) mf.A[e] = m.A[e] = finite(expf(m.A[e]));
     if (M > 1) fwd[set][sw][lane] = mf;
-    float mu[V];
+    float mu[V], h[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) h[e] = kept.v[e];
+    const size_t out = at;
+    const int have = cnt;
+    ti -= int(n);
+    if (first + int(n) < tiles) place();
     scan_exchange<V>(ex, set, m, carry, mu, w, lane, rank, n);
     float hp[S][V];  // h before each token
-    float h[V];
-#pragma unroll
-    for (int e = 0; e < V; ++e) h[e] = hc.v[e];
     if (M > 1) {
 #pragma unroll
       for (int i = 0; i < M - 1; ++i)
@@ -352,8 +437,8 @@ __global__ void __launch_bounds__(32 * kWarps, 4) scan_backward_kernel(const Sca
         dx[e] = BETA ? lam * to_f(b[i].v[e]) : lam;
         db[e] = lam * to_f(x[i].v[e]);
       }
-      if (on && i < cnt) {
-        const size_t o = at + (size_t)i * f.C;
+      if (on && i < have) {
+        const size_t o = out + (size_t)i * f.C;
         store<T, V>(static_cast<T*>(a.dx) + o, dx);
         store<float, V>(a.dg + o, dg);
         if (BETA) store<T, V>(static_cast<T*>(a.dbeta) + o, db);
@@ -394,11 +479,15 @@ int pick_cluster(const ScanArgs& a, int S, long long chains, int sms) {
 }
 
 template <typename Args>
-bool launch_cluster(void (*kernel)(const Args), const Args& args, long long ctas, int n,
-                    cudaStream_t stream) {
+bool launch_cluster(void (*kernel)(const Args), const Args& args, size_t smem, int slot,
+                    long long ctas, int n, cudaStream_t stream) {
+  if (smem > 48 * 1024 &&
+      !ensure_smem_attr(reinterpret_cast<const void*>(kernel), slot, int(smem)))
+    return false;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(unsigned(ctas * n));
   cfg.blockDim = dim3(32 * kWarps);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeClusterDimension;
@@ -415,9 +504,14 @@ int run_scan(ScanArgs a, int sms, cudaStream_t stream) {
   const long long chains = (long long)a.cblocks * a.N;
   if (chains * kMaxCluster > 0x7fffffffLL) return GDN_ERR_SHAPE;
   const int n = pick_cluster(a, S, chains, sms);
-  const bool ok = a.beta ? launch_cluster(&scan_kernel<T, V, S, true>, a, chains, n, stream)
-                         : launch_cluster(&scan_kernel<T, V, S, false>, a, chains, n, stream);
-  return ok ? GDN_OK : GDN_ERR_LAUNCH;
+  const auto go = [&](auto beta) {
+    constexpr bool kBeta = decltype(beta)::value;
+    constexpr size_t smem =
+        sizeof(Exchange<V>) + (kAsync<T, V> ? sizeof(Stage<T, V, S, kBeta ? 2 : 1>) : 0);
+    constexpr int slot = kScanSlot + (sizeof(T) == 4) * 4 + (V == 2) * 2 + kBeta;
+    return launch_cluster(&scan_kernel<T, V, S, kBeta>, a, smem, slot, chains, n, stream);
+  };
+  return (a.beta ? go(std::true_type{}) : go(std::false_type{})) ? GDN_OK : GDN_ERR_LAUNCH;
 }
 
 template <typename T, int V, int S>
@@ -427,10 +521,14 @@ int run_backward(ScanBackwardArgs a, int sms, cudaStream_t stream) {
   const long long chains = (long long)a.f.cblocks * a.f.N;
   if (chains * kMaxCluster > 0x7fffffffLL) return GDN_ERR_SHAPE;
   const int n = pick_cluster(a.f, S, chains, sms);
-  const bool ok =
-      a.f.beta ? launch_cluster(&scan_backward_kernel<T, V, S, true>, a, chains, n, stream)
-               : launch_cluster(&scan_backward_kernel<T, V, S, false>, a, chains, n, stream);
-  return ok ? GDN_OK : GDN_ERR_LAUNCH;
+  const auto go = [&](auto beta) {
+    constexpr bool kBeta = decltype(beta)::value;
+    constexpr size_t smem = sizeof(Exchange<V>) + sizeof(Map<V>[2][kWarps][32]) +
+                            (kAsync<T, V> ? sizeof(Stage<T, V, S, kBeta ? 3 : 2>) : 0);
+    constexpr int slot = kScanSlot + 8 + (sizeof(T) == 4) * 4 + (V == 2) * 2 + kBeta;
+    return launch_cluster(&scan_backward_kernel<T, V, S, kBeta>, a, smem, slot, chains, n, stream);
+  };
+  return (a.f.beta ? go(std::true_type{}) : go(std::false_type{})) ? GDN_OK : GDN_ERR_LAUNCH;
 }
 
 // Two channels a thread where the channel count is even and every array starts
