@@ -29,6 +29,7 @@
 
 #include "gdn_internal.h"
 #include "gdn_vec.cuh"
+#include "sm100.cuh"
 
 namespace gdn {
 namespace {
@@ -36,20 +37,38 @@ namespace {
 constexpr int kCarryTokens = GDN_SCAN_CARRY_TOKENS;
 constexpr int kWarps = 4;       // of a CTA, along time
 constexpr int kMaxCluster = 8;  // CTAs along time
+constexpr uint64_t kWaitLimitNs = 2000000000;  // of a wait for the cluster's maps
 constexpr int kScanSlot = 96;   // ensure_smem_attr: 16 kernels
 
 // The map of a run of tokens for V channels: c -> A c + H.  A stays finite, so
 // that a state of zero stays out of a run whose growth passes the fp32 range.
 template <int V>
 struct alignas(8 * V) Map {
-  float A[V], H[V];
+  F<V> A, H;
 };
-__device__ __forceinline__ float finite(float a) { return fminf(a, 3.402823466e38f); }
+template <int V>
+__device__ __forceinline__ F<V> finite(F<V> a) {
+#pragma unroll
+  for (int e = 0; e < V; ++e) a.v[e] = fminf(a.v[e], 3.402823466e38f);
+  return a;
+}
 
 template <int V>
-__device__ __forceinline__ void apply(const Map<V>& m, float (&c)[V]) {
+__device__ __forceinline__ F<V> apply(const Map<V>& m, F<V> c) {
+  return fma(m.A, c, m.H);
+}
+
+// exp(g) as 2^(g log2 e), the power by the approximate instruction (two units in
+// the last place; results below the normal range become zero).
+template <int V>
+__device__ __forceinline__ F<V> decay(F<V> g) {
+  F<V> k;
 #pragma unroll
-  for (int e = 0; e < V; ++e) c[e] = fmaf(m.A[e], c[e], m.H[e]);
+  for (int e = 0; e < V; ++e) k.v[e] = 1.4426950408889634f;
+  g = mul(g, k);
+#pragma unroll
+  for (int e = 0; e < V; ++e) asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(g.v[e]) : "f"(g.v[e]));
+  return g;
 }
 
 __device__ __forceinline__ unsigned cluster_size() {
@@ -66,18 +85,47 @@ __device__ __forceinline__ void cluster_barrier() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
                    : "memory");
 }
-// Stores a map to the same shared-memory address in CTA `rank` of the cluster.
+// Stores a map to the same shared-memory address in CTA `rank` of the cluster,
+// counted by that CTA's mbarrier.
 template <int V>
-__device__ __forceinline__ void store_remote(Map<V>* local, unsigned rank, const Map<V>& m) {
-  unsigned a = static_cast<unsigned>(__cvta_generic_to_shared(local)), b;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(b) : "r"(a), "r"(rank));
+__device__ __forceinline__ void store_remote(Map<V>* local, uint64_t* bar, unsigned rank,
+                                             const Map<V>& m) {
+  unsigned a, b;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+               : "=r"(a)
+               : "r"(static_cast<unsigned>(__cvta_generic_to_shared(local))), "r"(rank));
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+               : "=r"(b)
+               : "r"(static_cast<unsigned>(__cvta_generic_to_shared(bar))), "r"(rank));
   if constexpr (V == 2)
-    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(b), "f"(m.A[0]),
-                 "f"(m.A[1]), "f"(m.H[0]), "f"(m.H[1])
-                 : "memory");
+    asm volatile(
+        "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%2, %3, %4, %5}, "
+        "[%1];" ::"r"(a),
+        "r"(b), "f"(m.A.v[0]), "f"(m.A.v[1]), "f"(m.H.v[0]), "f"(m.H.v[1])
+        : "memory");
   else
-    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(b), "f"(m.A[0]), "f"(m.H[0])
-                 : "memory");
+    asm volatile(
+        "st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%2, %3}, [%1];" ::"r"(
+            a),
+        "r"(b), "f"(m.A.v[0]), "f"(m.H.v[0])
+        : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint64_t* bar, unsigned bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(
+                   static_cast<unsigned>(__cvta_generic_to_shared(bar))),
+               "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ bool bar_ready(uint64_t* bar, unsigned parity) {
+  unsigned ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok)
+      : "r"(static_cast<unsigned>(__cvta_generic_to_shared(bar))), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
 
 struct Seq {
@@ -102,58 +150,92 @@ __device__ __forceinline__ bool sequence(const ScanArgs& a, int n, Seq* s) {
   return true;
 }
 
-// Shared memory of the exchange: two sets, used in turn, so that one barrier a
-// cluster-tile is enough (a set is written again only behind the next one's).
+// Shared memory of the exchange: two sets, used in turn.  A set is written again
+// only behind the wait for the other one, which every thread that reads it has
+// passed by then (in this CTA by __syncthreads, in the cluster because a CTA
+// sends the next tile's map only after that barrier).
 template <int V>
 struct Exchange {
+  uint64_t bar[2];                 // the cluster's maps of a set have arrived
+  int pad[4];
   Map<V> warp[2][kWarps][32];      // this CTA's slices, in scan order
   Map<V> cta[2][kMaxCluster][32];  // the cluster's tiles, in scan order
 };
 
+// Before the first exchange.
+template <int V>
+__device__ __forceinline__ void exchange_init(Exchange<V>& ex, unsigned n) {
+  if (n == 1) return;
+  if (threadIdx.x == 0) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(
+                       static_cast<unsigned>(__cvta_generic_to_shared(&ex.bar[i])))
+                   : "memory");
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  cluster_barrier();  // every CTA runs, its barriers ready, before it is written to
+}
+
 // Shares the map of this thread's slice (scan order: CTA `rank`, warp `w`) and
 // turns carry, the state before the cluster-tile, into the state before the
-// slice (returned in c) and the state behind the cluster-tile (carry).
+// slice (returned in c) and the state behind the cluster-tile (carry).  `round`
+// counts the cluster-tiles.  Maps travel by st.async, counted by the receiver's
+// mbarrier: a cluster barrier's release would wait for all of the CTA's stores
+// to global memory as well.  The wait is bounded; a CTA that gave up once
+// (*late) waits no more, goes on with what it has and reports it at the end.
 template <int V>
-__device__ __forceinline__ void scan_exchange(Exchange<V>& ex, int set, const Map<V>& mine,
-                                              float (&carry)[V], float (&c)[V], int w, int lane,
-                                              unsigned rank, unsigned n) {
+__device__ __forceinline__ void scan_exchange(Exchange<V>& ex, int round, const Map<V>& mine,
+                                              F<V>& carry, F<V>& c, int w, int lane,
+                                              unsigned rank, unsigned n, bool* late) {
+  const int set = round & 1;
   ex.warp[set][w][lane] = mine;
+  if (n > 1 && threadIdx.x == 0 && !*late) bar_expect(&ex.bar[set], n * 32 * sizeof(Map<V>));
   __syncthreads();
-#pragma unroll
-  for (int e = 0; e < V; ++e) c[e] = carry[e];
+  c = carry;
   if (n > 1) {
     if (w < n) {  // warp w composes the CTA's map for the CTAs w, w + kWarps, ...
       Map<V> m = ex.warp[set][0][lane];
 #pragma unroll
       for (int i = 1; i < kWarps; ++i) {
         const Map<V> y = ex.warp[set][i][lane];
-        apply(y, m.H);
-#pragma unroll
-        for (int e = 0; e < V; ++e) m.A[e] = finite(m.A[e] * y.A[e]);
+        m.H = apply(y, m.H);
+        m.A = finite(mul(m.A, y.A));
       }
-      for (unsigned r = w; r < n; r += kWarps) store_remote(&ex.cta[set][rank][lane], r, m);
+      for (unsigned r = w; r < n; r += kWarps)
+        store_remote(&ex.cta[set][rank][lane], &ex.bar[set], r, m);
     }
-    cluster_barrier();
+    const unsigned parity = (round >> 1) & 1;
+    if (!*late && !bar_ready(&ex.bar[set], parity)) {
+      const uint64_t begin = sm100::globaltimer_ns();
+      unsigned polls = 0;
+      while (!bar_ready(&ex.bar[set], parity))
+        if ((++polls & 255u) == 0 && sm100::globaltimer_ns() - begin > kWaitLimitNs) {
+          *late = true;
+          break;
+        }
+    }
     for (unsigned r = 0; r < n; ++r) {
-      if (r == rank) {
-#pragma unroll
-        for (int e = 0; e < V; ++e) c[e] = carry[e];
-      }
-      apply(ex.cta[set][r][lane], carry);
+      if (r == rank) c = carry;
+      carry = apply(ex.cta[set][r][lane], carry);
     }
 #pragma unroll
     for (int i = 0; i < kWarps - 1; ++i)
-      if (i < w) apply(ex.warp[set][i][lane], c);
+      if (i < w) c = apply(ex.warp[set][i][lane], c);
   } else {
 #pragma unroll
     for (int i = 0; i < kWarps; ++i) {
-      if (i == w) {
-#pragma unroll
-        for (int e = 0; e < V; ++e) c[e] = carry[e];
-      }
-      apply(ex.warp[set][i][lane], carry);
+      if (i == w) c = carry;
+      carry = apply(ex.warp[set][i][lane], carry);
     }
   }
+}
+
+// Behind the last exchange: no CTA ends while another may still write to it.
+__device__ __forceinline__ void exchange_end(unsigned n, bool late, int* status) {
+  if (n == 1) return;
+  if (late && status) *status = GDN_ERR_DEVICE_TIMEOUT;
+  cluster_barrier();
 }
 
 // A thread's slice on its way from memory: the log decays and K arrays of T, copied
@@ -212,8 +294,6 @@ __device__ __forceinline__ void take(E (&r)[S], const E (&src)[S][32 * kWarps], 
   }
 }
 
-__device__ __forceinline__ float decay(float g) { return __expf(g); }
-
 template <typename T, int V, int S, bool BETA>
 __global__ void __launch_bounds__(32 * kWarps, 4) scan_kernel(const ScanArgs a) {
   constexpr bool kStaged = kAsync<T, V>;
@@ -231,15 +311,9 @@ __global__ void __launch_bounds__(32 * kWarps, 4) scan_kernel(const ScanArgs a) 
     if (a.status && threadIdx.x == 0 && rank == 0) *a.status = GDN_ERR_SHAPE;
     return;
   }
-  if (n > 1) cluster_barrier();  // every CTA runs before its shared memory is written
-  float carry[V];
-#pragma unroll
-  for (int e = 0; e < V; ++e) carry[e] = 0.f;
-  if (a.h0) {
-    const Vec<float, V> v = load<float, V>(a.h0 + (size_t)seq * a.C + c0);
-#pragma unroll
-    for (int e = 0; e < V; ++e) carry[e] = v.v[e];
-  }
+  exchange_init(ex, n);
+  F<V> carry{};
+  if (a.h0) carry = to_f(load<float, V>(a.h0 + (size_t)seq * a.C + c0));
   constexpr int tile = kWarps * S;
   const int step = tile * int(n);
   const size_t gs = size_t(a.C) * 4, ts = size_t(a.C) * sizeof(T);
@@ -260,56 +334,51 @@ __global__ void __launch_bounds__(32 * kWarps, 4) scan_kernel(const ScanArgs a) 
     }
   };
   if (s.len > 0) place();
-  int set = 0;
-  for (int base = 0; base < s.len; base += step, set ^= 1) {
+  int round = 0;
+  bool late = false;
+  for (int base = 0; base < s.len; base += step, ++round) {
     if (kStaged) copies_done();
     Vec<float, V> g[S];
     Vec<T, V> x[S], b[S];
     take<kStaged>(g, st.g, pg, gs, cnt);
     take<kStaged>(x, st.t[0], px, ts, cnt);
     if (BETA) take<kStaged>(b, st.t[BETA ? 1 : 0], pb, ts, cnt);
-    float al[S][V], u[S][V], h[V];
-    Map<V> m;
-#pragma unroll
-    for (int e = 0; e < V; ++e) m.A[e] = m.H[e] = 0.f;
-#pragma unroll
-    for (int i = 0; i < S; ++i)
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        al[i][e] = decay(g[i].v[e]);
-        u[i][e] = BETA ? to_f(x[i].v[e]) * to_f(b[i].v[e]) : to_f(x[i].v[e]);
-        m.A[e] += g[i].v[e];
-        m.H[e] = fmaf(al[i][e], m.H[e], u[i][e]);
-      }
-#pragma unroll
-    for (int e = 0; e < V; ++e) m.A[e] = finite(expf(m.A[e]));
     const int now = t0, have = cnt;
     t0 += step;
-    if (base + step < s.len) place();  // in flight through the exchange and the stores
-    scan_exchange<V>(ex, set, m, carry, h, w, lane, rank, n);
+    if (base + step < s.len) place();  // in flight while this slice is worked on
+    F<V> al[S], u[S], h;
+    Map<V> m{};
+#pragma unroll
+    for (int i = 0; i < S; ++i) {
+      al[i] = decay(to_f(g[i]));
+      u[i] = BETA ? mul(to_f(x[i]), to_f(b[i])) : to_f(x[i]);
+      m.A = add(m.A, to_f(g[i]));
+      m.H = fma(al[i], m.H, u[i]);
+    }
+    m.A = finite(decay(m.A));
+    scan_exchange<V>(ex, round, m, carry, h, w, lane, rank, n, &late);
     if (have > 0 && on && a.carries && now % kCarryTokens == 0)
-      store<float, V>(a.carries + size_t(s.carry_row + now / kCarryTokens) * a.C + c0, h);
+      store<float, V>(a.carries + size_t(s.carry_row + now / kCarryTokens) * a.C + c0, h.v);
     if (a.h && on) {
       T* ph = static_cast<T*>(a.h) + (have > 0 ? size_t(s.start + now) * a.C + c0 : 0);
       if (have == S) {
 #pragma unroll
         for (int i = 0; i < S; ++i) {
-#pragma unroll
-          for (int e = 0; e < V; ++e) h[e] = fmaf(al[i][e], h[e], u[i][e]);
-          store<T, V>(ph + (size_t)i * a.C, h);
+          h = fma(al[i], h, u[i]);
+          store<T, V>(ph + (size_t)i * a.C, h.v);
         }
       } else {
 #pragma unroll
         for (int i = 0; i < S; ++i) {
-#pragma unroll
-          for (int e = 0; e < V; ++e) h[e] = fmaf(al[i][e], h[e], u[i][e]);
-          if (i < have) store<T, V>(ph + (size_t)i * a.C, h);
+          h = fma(al[i], h, u[i]);
+          if (i < have) store<T, V>(ph + (size_t)i * a.C, h.v);
         }
       }
     }
   }
   if (a.h_T && rank == 0 && w == 0 && on)
-    store<float, V>(a.h_T + (size_t)seq * a.C + c0, carry);
+    store<float, V>(a.h_T + (size_t)seq * a.C + c0, carry.v);
+  exchange_end(n, late, a.status);
 }
 
 // Backward: the same walk from the sequence's end.  What passes a token
@@ -338,15 +407,9 @@ __global__ void __launch_bounds__(32 * kWarps, 4) scan_backward_kernel(const Sca
     if (f.status && threadIdx.x == 0 && rank == 0) *f.status = GDN_ERR_SHAPE;
     return;
   }
-  if (n > 1) cluster_barrier();
-  float carry[V];
-#pragma unroll
-  for (int e = 0; e < V; ++e) carry[e] = 0.f;
-  if (a.dh_T) {
-    const Vec<float, V> v = load<float, V>(a.dh_T + (size_t)seq * f.C + c0);
-#pragma unroll
-    for (int e = 0; e < V; ++e) carry[e] = v.v[e];
-  }
+  exchange_init(ex, n);
+  F<V> carry{};
+  if (a.dh_T) carry = to_f(load<float, V>(a.dh_T + (size_t)seq * f.C + c0));
   constexpr int tile = kWarps * S;
   const int tiles = (s.len + tile - 1) / tile;
   const int sw = kWarps - 1 - w;  // scan order runs backwards in time
@@ -373,8 +436,10 @@ __global__ void __launch_bounds__(32 * kWarps, 4) scan_backward_kernel(const Sca
       kept = load<float, V>(f.carries + size_t(s.carry_row + t0 / kCarryTokens) * f.C + c0);
   };
   if (tiles > 0) place();
-  int set = 0;
-  for (int first = 0; first < tiles; first += int(n), set ^= 1) {
+  int round = 0;
+  bool late = false;
+  for (int first = 0; first < tiles; first += int(n), ++round) {
+    const int set = round & 1;
     if (kStaged) copies_done();
     Vec<float, V> g[S];
     Vec<T, V> x[S], b[S], d[S];
@@ -382,71 +447,51 @@ __global__ void __launch_bounds__(32 * kWarps, 4) scan_backward_kernel(const Sca
     take<kStaged>(d, st.t[0], pd, ts, cnt);
     take<kStaged>(x, st.t[1], px, ts, cnt);
     if (BETA) take<kStaged>(b, st.t[BETA ? 2 : 0], pb, ts, cnt);
-    float al[S][V];
-    Map<V> m, mf;
-#pragma unroll
-    for (int e = 0; e < V; ++e) m.A[e] = m.H[e] = mf.H[e] = 0.f;
-#pragma unroll
-    for (int i = 0; i < S; ++i)
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        al[i][e] = decay(g[i].v[e]);
-        m.A[e] += g[i].v[e];
-        if (M > 1) {
-          const float u = BETA ? to_f(x[i].v[e]) * to_f(b[i].v[e]) : to_f(x[i].v[e]);
-          mf.H[e] = fmaf(al[i][e], mf.H[e], u);
-        }
-      }
-#pragma unroll
-    for (int i = S - 1; i >= 0; --i)
-#pragma unroll
-      for (int e = 0; e < V; ++e) m.H[e] = al[i][e] * (to_f(d[i].v[e]) + m.H[e]);
-#pragma unroll
-    for (int e = 0; e < V; ++e) mf.A[e] = m.A[e] = finite(expf(m.A[e]));
-    if (M > 1) fwd[set][sw][lane] = mf;
-    float mu[V], h[V];
-#pragma unroll
-    for (int e = 0; e < V; ++e) h[e] = kept.v[e];
+    F<V> h = to_f(kept), mu;
     const size_t out = at;
     const int have = cnt;
     ti -= int(n);
     if (first + int(n) < tiles) place();
-    scan_exchange<V>(ex, set, m, carry, mu, w, lane, rank, n);
-    float hp[S][V];  // h before each token
+    const auto input = [&](int i) { return BETA ? mul(to_f(x[i]), to_f(b[i])) : to_f(x[i]); };
+    F<V> al[S];
+    Map<V> m{}, mf{};
+#pragma unroll
+    for (int i = 0; i < S; ++i) {
+      al[i] = decay(to_f(g[i]));
+      m.A = add(m.A, to_f(g[i]));
+      if (M > 1) mf.H = fma(al[i], mf.H, input(i));
+    }
+#pragma unroll
+    for (int i = S - 1; i >= 0; --i) m.H = mul(al[i], add(to_f(d[i]), m.H));
+    mf.A = m.A = finite(decay(m.A));
+    if (M > 1) fwd[set][sw][lane] = mf;
+    scan_exchange<V>(ex, round, m, carry, mu, w, lane, rank, n, &late);
     if (M > 1) {
 #pragma unroll
       for (int i = 0; i < M - 1; ++i)
-        if (i < sw % M) apply(fwd[set][sw - sw % M + i][lane], h);
+        if (i < sw % M) h = apply(fwd[set][sw - sw % M + i][lane], h);
+    }
+    F<V> hp[S];  // h before each token
+#pragma unroll
+    for (int i = 0; i < S; ++i) {
+      hp[i] = h;
+      h = fma(al[i], h, input(i));
     }
 #pragma unroll
-    for (int i = 0; i < S; ++i)
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        hp[i][e] = h[e];
-        const float u = BETA ? to_f(x[i].v[e]) * to_f(b[i].v[e]) : to_f(x[i].v[e]);
-        h[e] = fmaf(al[i][e], h[e], u);
-      }
-#pragma unroll
     for (int i = S - 1; i >= 0; --i) {
-      float dx[V], db[V], dg[V];
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float lam = to_f(d[i].v[e]) + mu[e];
-        mu[e] = al[i][e] * lam;
-        dg[e] = mu[e] * hp[i][e];
-        dx[e] = BETA ? lam * to_f(b[i].v[e]) : lam;
-        db[e] = lam * to_f(x[i].v[e]);
-      }
+      const F<V> lam = add(to_f(d[i]), mu);
+      mu = mul(al[i], lam);
       if (on && i < have) {
         const size_t o = out + (size_t)i * f.C;
-        store<T, V>(static_cast<T*>(a.dx) + o, dx);
-        store<float, V>(a.dg + o, dg);
-        if (BETA) store<T, V>(static_cast<T*>(a.dbeta) + o, db);
+        store<T, V>(static_cast<T*>(a.dx) + o, (BETA ? mul(lam, to_f(b[i])) : lam).v);
+        store<float, V>(a.dg + o, mul(mu, hp[i]).v);
+        if (BETA) store<T, V>(static_cast<T*>(a.dbeta) + o, mul(lam, to_f(x[i])).v);
       }
     }
   }
   if (a.dh0 && rank == 0 && w == 0 && on)
-    store<float, V>(a.dh0 + (size_t)seq * f.C + c0, carry);
+    store<float, V>(a.dh0 + (size_t)seq * f.C + c0, carry.v);
+  exchange_end(n, late, f.status);
 }
 
 // One token: elementwise, V channels a thread.
