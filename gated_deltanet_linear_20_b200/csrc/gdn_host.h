@@ -1,8 +1,11 @@
 // Host-side checks shared by the C-ABI files.
 #pragma once
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
+
+#include <cuda_runtime.h>
 
 namespace gdn {
 
@@ -34,6 +37,23 @@ inline bool any_alias(const Span* outs, int n_out, const Span* ins, int n_in, co
       if (overlaps(outs[i].p, outs[i].bytes, outs[j].p, outs[j].bytes)) return true;
   }
   return false;
+}
+
+// Raises a kernel's dynamic shared-memory limit once per device to `most` bytes
+// (up to 32 KB need no raising beside at most 16 KB of static shared memory).
+template <auto Kernel>
+bool raise_smem(size_t most) {
+  static std::atomic<uint64_t> done{0};  // bit d: device d
+  int dev = 0;
+  if (most <= 32 * 1024) return true;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+  const uint64_t bit = uint64_t(1) << dev;
+  if (done.load(std::memory_order_acquire) & bit) return true;
+  if (cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(most)) !=
+      cudaSuccess)
+    return false;
+  done.fetch_or(bit, std::memory_order_acq_rel);
+  return true;
 }
 
 // The current device must be compute capability 10.0; *sms is its SM count.

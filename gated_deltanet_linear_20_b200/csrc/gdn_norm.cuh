@@ -5,6 +5,11 @@
 // vectors of V channels each (vector j of thread t: channels (j TPR + t) V ..),
 // so it is read from memory once, whatever is summed over it.  Sub-warp rows
 // (TPR 8, 16, 32) share a CTA and sum by shuffles; longer ones have a CTA.
+//
+// CTAs are persistent, and each thread copies its part of the next rows to shared
+// memory asynchronously (a ring of two or three stages) while it works on the present one:
+// the sums over a row and their barriers would leave the memory idle otherwise.
+// A thread reads only what it copied, so the ring needs no barrier.
 #pragma once
 
 #include <algorithm>
@@ -53,6 +58,44 @@ __device__ __forceinline__ void gate_slope(int act, float z, float* a, float* da
   const float p = sigmoid(z);
   *a = act == GDN_GATE_SILU ? z * p : p;
   *da = act == GDN_GATE_SILU ? p * (1.f + z * (1.f - p)) : p * (1.f - p);
+}
+
+// Stages of a ring whose arrays have `bytes` a channel in all: three, if the
+// longest staged row leaves room for them.
+constexpr int stages(size_t bytes) { return bytes * 8 * kNormMaxThreads * 3 <= 220 * 1024 ? 3 : 2; }
+// Staged layouts: vectors of four (cp.async moves at least 4 bytes), up to two a
+// thread (larger rows would not fit the ring).
+template <int NV, int V>
+constexpr bool kStaged = V == 4 && NV <= 2;
+
+// The ring of one array: NV vectors of each thread in each stage.
+template <typename T, int V, int NV, int kStages>
+struct Ring {
+  Vec<T, V>* at;
+  __device__ __forceinline__ Ring(unsigned char*& smem) : at(reinterpret_cast<Vec<T, V>*>(smem)) {
+    smem += sizeof(Vec<T, V>) * NV * kStages * blockDim.x;
+  }
+  __device__ __forceinline__ Vec<T, V>* slot(int stage, int j) const {
+    return at + (stage * NV + j) * blockDim.x + threadIdx.x;
+  }
+  // channels c >= D are zeros (D = 0: all of them, nothing is read)
+  __device__ __forceinline__ void fetch(int stage, const T* p, int t, int tpr, int D) const {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * tpr + t) * V;
+      copy_async(slot(stage, j), reinterpret_cast<const Vec<T, V>*>(c < D ? p + c : p),
+                 c < D ? int(sizeof(Vec<T, V>)) : 0);
+    }
+  }
+  __device__ __forceinline__ void take(Vec<T, V> (&r)[NV], int stage) const {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) r[j] = *slot(stage, j);
+  }
+};
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kStages>
+__device__ __forceinline__ void copies_wait() {  // for the oldest stage in flight
+  asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
 }
 
 template <typename T, int V, int NV>
@@ -121,17 +164,18 @@ __device__ __forceinline__ void store_partial(float* part, const float (&acc)[NV
 }
 
 // Calls f.template run<TPR, NV, V>() with the layout for rows of D channels:
-// 16-byte accesses where D is a multiple of 8 and every array starts on 16
-// bytes (`wide`), else single elements.  TPR 0: one CTA a row.
+// vectors of four where D is a multiple of 4 and every array starts on one
+// (`wide`: 8 bytes of bf16, 16 of fp32), else single elements.  TPR 0: one CTA a
+// row.
 template <typename F>
 int with_layout(int D, bool wide, F&& f) {
-  if (wide && D % 8 == 0) {
-    if (D <= 64) return f.template run<8, 1, 8>();
-    if (D <= 128) return f.template run<16, 1, 8>();
-    if (D <= 256) return f.template run<32, 1, 8>();
-    if (D <= 8 * kNormMaxThreads) return f.template run<0, 1, 8>();
-    if (D <= 16 * kNormMaxThreads) return f.template run<0, 2, 8>();
-    return f.template run<0, 4, 8>();
+  if (wide && D % 4 == 0) {
+    if (D <= 64) return f.template run<8, 2, 4>();
+    if (D <= 128) return f.template run<16, 2, 4>();
+    if (D <= 256) return f.template run<32, 2, 4>();
+    if (D <= 8 * kNormMaxThreads) return f.template run<0, 2, 4>();
+    if (D <= 16 * kNormMaxThreads) return f.template run<0, 4, 4>();
+    return f.template run<0, 8, 4>();
   }
   if (D <= 256) return f.template run<32, 8, 1>();
   if (D <= 8 * kNormMaxThreads) return f.template run<0, 8, 1>();

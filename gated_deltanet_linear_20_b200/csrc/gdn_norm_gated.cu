@@ -9,6 +9,7 @@
 // directions.  The backward pass finds rstd and mean(u xh) in one sum over the
 // row (sum x^2 and sum u x), and keeps dw in registers while a CTA walks its
 // rows; the CTAs' partial sums are added by a second launch in a fixed order.
+#include "gdn_host.h"
 #include "gdn_norm.cuh"
 
 namespace gdn {
@@ -24,16 +25,45 @@ __global__ void __launch_bounds__(TPR ? kNormThreads : kNormMaxThreads)
   float w[NV][V];
   load_weight<V, NV>(w, a.w, a.offset, 1.f, t, tpr, a.D);
   const float inv = 1.f / float(a.D);
-  for (long long row0 = (long long)blockIdx.x * per; row0 < a.rows;
-       row0 += (long long)gridDim.x * per) {
-    const long long row = row0 + threadIdx.x / tpr;
+  constexpr int kStages = stages(sizeof(TX) + sizeof(T));
+  extern __shared__ __align__(16) unsigned char smem[];
+  [[maybe_unused]] unsigned char* top = smem;
+  [[maybe_unused]] const Ring<TX, V, NV, kStages> rx(top);
+  [[maybe_unused]] const Ring<T, V, NV, kStages> rz(top);
+  const long long stride = (long long)gridDim.x * per;
+  const int sub = threadIdx.x / tpr;
+  const auto fetch = [&](int stage, long long row) {
+    if constexpr (kStaged<NV, V>) {
+      if (row < a.rows + per) {  // (a whole CTA's rows past the end: nothing to copy)
+        const int D = row < a.rows ? a.D : 0;
+        const size_t at = size_t(row < a.rows ? row : 0) * a.D;
+        rx.fetch(stage, static_cast<const TX*>(a.x) + at, t, tpr, D);
+        if (a.z) rz.fetch(stage, static_cast<const T*>(a.z) + at, t, tpr, D);
+      }
+      copies_commit();
+    }
+  };
+  const long long first = (long long)blockIdx.x * per;
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) fetch(i, first + i * stride + sub);
+  int stage = 0;
+  for (long long row0 = first; row0 < a.rows; row0 += stride) {
+    const long long row = row0 + sub;
     const bool on = row < a.rows;
     const size_t at = size_t(on ? row : 0) * a.D;
     const int D = on ? a.D : 0;
     Vec<TX, V> x[NV];
     Vec<T, V> z[NV];
-    load_row<TX, V, NV>(x, static_cast<const TX*>(a.x) + at, t, tpr, D);
-    if (a.z) load_row<T, V, NV>(z, static_cast<const T*>(a.z) + at, t, tpr, D);
+    if constexpr (kStaged<NV, V>) {
+      copies_wait<kStages>();
+      rx.take(x, stage);
+      if (a.z) rz.take(z, stage);
+      fetch(stage == 0 ? kStages - 1 : stage - 1, row + (kStages - 1) * stride);
+      stage = stage == kStages - 1 ? 0 : stage + 1;
+    } else {
+      load_row<TX, V, NV>(x, static_cast<const TX*>(a.x) + at, t, tpr, D);
+      if (a.z) load_row<T, V, NV>(z, static_cast<const T*>(a.z) + at, t, tpr, D);
+    }
     float s[1] = {0.f};
 #pragma unroll
     for (int j = 0; j < NV; ++j)
@@ -68,17 +98,49 @@ __global__ void __launch_bounds__(TPR ? kNormThreads : kNormMaxThreads)
 #pragma unroll
     for (int e = 0; e < V; ++e) dw[j][e] = 0.f;
   const float inv = 1.f / float(a.D);
-  for (long long row0 = (long long)blockIdx.x * per; row0 < a.rows;
-       row0 += (long long)gridDim.x * per) {
-    const long long row = row0 + threadIdx.x / tpr;
+  constexpr int kStages = stages(sizeof(TX) + 2 * sizeof(T));
+  extern __shared__ __align__(16) unsigned char smem[];
+  [[maybe_unused]] unsigned char* top = smem;
+  [[maybe_unused]] const Ring<TX, V, NV, kStages> rx(top);
+  [[maybe_unused]] const Ring<T, V, NV, kStages> rd(top);
+  [[maybe_unused]] const Ring<T, V, NV, kStages> rz(top);
+  const long long stride = (long long)gridDim.x * per;
+  const int sub = threadIdx.x / tpr;
+  const auto fetch = [&](int stage, long long row) {
+    if constexpr (kStaged<NV, V>) {
+      if (row < a.rows + per) {  // (a whole CTA's rows past the end: nothing to copy)
+        const int D = row < a.rows ? a.D : 0;
+        const size_t at = size_t(row < a.rows ? row : 0) * a.D;
+        rx.fetch(stage, static_cast<const TX*>(a.x) + at, t, tpr, D);
+        rd.fetch(stage, static_cast<const T*>(a.dy) + at, t, tpr, D);
+        if (a.z) rz.fetch(stage, static_cast<const T*>(a.z) + at, t, tpr, D);
+      }
+      copies_commit();
+    }
+  };
+  const long long first = (long long)blockIdx.x * per;
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) fetch(i, first + i * stride + sub);
+  int stage = 0;
+  for (long long row0 = first; row0 < a.rows; row0 += stride) {
+    const long long row = row0 + sub;
     const bool on = row < a.rows;
     const size_t at = size_t(on ? row : 0) * a.D;
     const int D = on ? a.D : 0;
     Vec<TX, V> x[NV];
     Vec<T, V> z[NV], dy[NV];
-    load_row<TX, V, NV>(x, static_cast<const TX*>(a.x) + at, t, tpr, D);
-    load_row<T, V, NV>(dy, static_cast<const T*>(a.dy) + at, t, tpr, D);
-    if (a.z) load_row<T, V, NV>(z, static_cast<const T*>(a.z) + at, t, tpr, D);
+    if constexpr (kStaged<NV, V>) {
+      copies_wait<kStages>();
+      rx.take(x, stage);
+      rd.take(dy, stage);
+      if (a.z) rz.take(z, stage);
+      fetch(stage == 0 ? kStages - 1 : stage - 1, row + (kStages - 1) * stride);
+      stage = stage == kStages - 1 ? 0 : stage + 1;
+    } else {
+      load_row<TX, V, NV>(x, static_cast<const TX*>(a.x) + at, t, tpr, D);
+      load_row<T, V, NV>(dy, static_cast<const T*>(a.dy) + at, t, tpr, D);
+      if (a.z) load_row<T, V, NV>(z, static_cast<const T*>(a.z) + at, t, tpr, D);
+    }
     float u[NV][V], dz[NV][V], s[2] = {0.f, 0.f};
 #pragma unroll
     for (int j = 0; j < NV; ++j)
@@ -112,6 +174,8 @@ __global__ void __launch_bounds__(TPR ? kNormThreads : kNormMaxThreads)
     store_partial<TPR, V, NV>(a.part + size_t(blockIdx.x) * a.D, dw, groups, t, tpr, a.D);
 }
 
+constexpr long long kForwardCtas = 8;  // per SM
+
 template <typename TX, typename T>
 struct Forward {
   const GatedNormArgs& a;
@@ -121,8 +185,12 @@ struct Forward {
   int run() {
     const int threads = norm_threads<TPR, NV, V>(a.D), per = TPR ? kNormThreads / TPR : 1;
     const long long groups = (a.rows + per - 1) / per;
-    const int grid = int(groups < 8LL * sms ? groups : 8LL * sms);
-    gated_norm_kernel<TPR, NV, V, TX, T><<<grid, threads, 0, stream>>>(a);
+    const int grid = int(groups < kForwardCtas * sms ? groups : kForwardCtas * sms);
+    constexpr size_t kBytes = sizeof(TX) + sizeof(T);  // staged of a channel
+    constexpr size_t kThread = kStaged<NV, V> ? stages(kBytes) * NV * V * kBytes : 0;
+    constexpr int kMost = TPR ? kNormThreads : kNormMaxThreads;
+    if (!raise_smem<&gated_norm_kernel<TPR, NV, V, TX, T>>(kThread * kMost)) return GDN_ERR_LAUNCH;
+    gated_norm_kernel<TPR, NV, V, TX, T><<<grid, threads, kThread * threads, stream>>>(a);
     return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_LAUNCH;
   }
 };
@@ -138,7 +206,11 @@ struct Backward {
     const long long groups = (a.rows + per - 1) / per;
     const int most = norm_max_parts(a.rows, a.D);
     const int grid = int(groups < most ? groups : most);
-    gated_norm_backward_kernel<TPR, NV, V, TX, T><<<grid, threads, 0, stream>>>(a);
+    constexpr size_t kBytes = sizeof(TX) + 2 * sizeof(T);  // staged of a channel
+    constexpr size_t kThread = kStaged<NV, V> ? stages(kBytes) * NV * V * kBytes : 0;
+    constexpr int kMost = TPR ? kNormThreads : kNormMaxThreads;
+    if (!raise_smem<&gated_norm_backward_kernel<TPR, NV, V, TX, T>>(kThread * kMost)) return GDN_ERR_LAUNCH;
+    gated_norm_backward_kernel<TPR, NV, V, TX, T><<<grid, threads, kThread * threads, stream>>>(a);
     if (cudaGetLastError() != cudaSuccess) return GDN_ERR_LAUNCH;
     return launch_reduce_parts(a.part, grid, a.D, &a.dw, a.D, stream);
   }

@@ -12,6 +12,7 @@
 // only inputs in the first sum).  y comes from the fp32 sum before r' is rounded
 // to its type.  The weight gradients of a CTA's rows stay in registers and the
 // CTAs' partial sums are added by a second launch in a fixed order.
+#include "gdn_host.h"
 #include "gdn_norm.cuh"
 
 namespace gdn {
@@ -33,17 +34,49 @@ __global__ void __launch_bounds__(TPR ? kNormThreads : kNormMaxThreads)
 #pragma unroll
     for (int e = 0; e < V; ++e) wp[j][e] *= sc[j][e];
   const float inv = 1.f / float(a.D);
-  for (long long row0 = (long long)blockIdx.x * per; row0 < a.rows;
-       row0 += (long long)gridDim.x * per) {
-    const long long row = row0 + threadIdx.x / tpr;
+  constexpr int kStages = stages(2 * sizeof(T) + sizeof(TR));
+  extern __shared__ __align__(16) unsigned char smem[];
+  [[maybe_unused]] unsigned char* top = smem;
+  [[maybe_unused]] const Ring<TR, V, NV, kStages> rr(top);
+  [[maybe_unused]] const Ring<T, V, NV, kStages> rx(top);
+  [[maybe_unused]] const Ring<T, V, NV, kStages> rz(top);
+  const long long stride = (long long)gridDim.x * per;
+  const int sub = threadIdx.x / tpr;
+  const auto fetch = [&](int stage, long long row) {
+    if constexpr (kStaged<NV, V>) {
+      if (row < a.rows + per) {  // (a whole CTA's rows past the end: nothing to copy)
+        const int D = row < a.rows ? a.D : 0;
+        const size_t at = size_t(row < a.rows ? row : 0) * a.D;
+        rx.fetch(stage, static_cast<const T*>(a.x) + at, t, tpr, D);
+        rr.fetch(stage, static_cast<const TR*>(a.r) + at, t, tpr, D);
+        if (a.z) rz.fetch(stage, static_cast<const T*>(a.z) + at, t, tpr, D);
+      }
+      copies_commit();
+    }
+  };
+  const long long first = (long long)blockIdx.x * per;
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) fetch(i, first + i * stride + sub);
+  int stage = 0;
+  for (long long row0 = first; row0 < a.rows; row0 += stride) {
+    const long long row = row0 + sub;
     const bool on = row < a.rows;
     const size_t at = size_t(on ? row : 0) * a.D;
     const int D = on ? a.D : 0;
     Vec<T, V> x[NV], z[NV];
     Vec<TR, V> r[NV];
-    load_row<T, V, NV>(x, static_cast<const T*>(a.x) + at, t, tpr, D);
-    load_row<TR, V, NV>(r, static_cast<const TR*>(a.r) + at, t, tpr, D);
-    if (a.z) load_row<T, V, NV>(z, static_cast<const T*>(a.z) + at, t, tpr, D);
+    if constexpr (kStaged<NV, V>) {
+      copies_wait<kStages>();
+      rx.take(x, stage);
+      rr.take(r, stage);
+      if (a.z) rz.take(z, stage);
+      fetch(stage == 0 ? kStages - 1 : stage - 1, row + (kStages - 1) * stride);
+      stage = stage == kStages - 1 ? 0 : stage + 1;
+    } else {
+      load_row<T, V, NV>(x, static_cast<const T*>(a.x) + at, t, tpr, D);
+      load_row<TR, V, NV>(r, static_cast<const TR*>(a.r) + at, t, tpr, D);
+      if (a.z) load_row<T, V, NV>(z, static_cast<const T*>(a.z) + at, t, tpr, D);
+    }
     float rstd = 1.f;
     if (a.w_post) {
       float s[1] = {0.f};
@@ -66,11 +99,11 @@ __global__ void __launch_bounds__(TPR ? kNormThreads : kNormMaxThreads)
       }
     store_row<TR, V, NV>(static_cast<TR*>(a.r_out) + at, q, t, tpr, D);
     row_sum<TPR, 1>(s, buf, turn);
-    const float rr = rsqrtf(fmaf(s[0], inv, a.eps));
+    const float rs = rsqrtf(fmaf(s[0], inv, a.eps));
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
-      for (int e = 0; e < V; ++e) q[j][e] *= rr * w[j][e];
+      for (int e = 0; e < V; ++e) q[j][e] *= rs * w[j][e];
     store_row<T, V, NV>(static_cast<T*>(a.y) + at, q, t, tpr, D);
   }
 }
@@ -92,19 +125,62 @@ __global__ void __launch_bounds__(TPR ? kNormThreads : kNormMaxThreads)
 #pragma unroll
     for (int e = 0; e < V; ++e) dw[j][e] = dwp[j][e] = dsc[j][e] = 0.f;
   const float inv = 1.f / float(a.D);
-  for (long long row0 = (long long)blockIdx.x * per; row0 < a.rows;
-       row0 += (long long)gridDim.x * per) {
-    const long long row = row0 + threadIdx.x / tpr;
+  constexpr int kStages = stages(3 * sizeof(T) + 2 * sizeof(TR));
+  extern __shared__ __align__(16) unsigned char smem[];
+  [[maybe_unused]] unsigned char* top = smem;
+  [[maybe_unused]] const Ring<TR, V, NV, kStages> rr(top);
+  [[maybe_unused]] const Ring<TR, V, NV, kStages> rg(top);
+  [[maybe_unused]] const Ring<T, V, NV, kStages> rd(top);
+  [[maybe_unused]] const Ring<T, V, NV, kStages> rx(top);
+  [[maybe_unused]] const Ring<T, V, NV, kStages> rz(top);
+  const long long stride = (long long)gridDim.x * per;
+  const int sub = threadIdx.x / tpr;
+  const auto fetch = [&](int stage, long long row) {
+    if constexpr (kStaged<NV, V>) {
+      if (row < a.rows + per) {  // (a whole CTA's rows past the end: nothing to copy)
+        const int D = row < a.rows ? a.D : 0;
+        const size_t at = size_t(row < a.rows ? row : 0) * a.D;
+        rr.fetch(stage, static_cast<const TR*>(a.r) + at, t, tpr, D);
+        rd.fetch(stage, static_cast<const T*>(a.dy) + at, t, tpr, D);
+        rx.fetch(stage, static_cast<const T*>(a.x) + at, t, tpr, D);
+        if (a.dr_out) rg.fetch(stage, static_cast<const TR*>(a.dr_out) + at, t, tpr, D);
+        if (a.z) rz.fetch(stage, static_cast<const T*>(a.z) + at, t, tpr, D);
+      }
+      copies_commit();
+    }
+  };
+  const long long first = (long long)blockIdx.x * per;
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) fetch(i, first + i * stride + sub);
+  int stage = 0;
+  for (long long row0 = first; row0 < a.rows; row0 += stride) {
+    const long long row = row0 + sub;
     const bool on = row < a.rows;
     const size_t at = size_t(on ? row : 0) * a.D;
     const int D = on ? a.D : 0;
     Vec<T, V> x[NV], z[NV], dy[NV];
     Vec<TR, V> r[NV], dr[NV];
-    load_row<TR, V, NV>(r, static_cast<const TR*>(a.r) + at, t, tpr, D);
-    load_row<T, V, NV>(dy, static_cast<const T*>(a.dy) + at, t, tpr, D);
-    load_row<T, V, NV>(x, static_cast<const T*>(a.x) + at, t, tpr, D);
-    load_row<TR, V, NV>(dr, static_cast<const TR*>(a.dr_out) + at, t, tpr, a.dr_out ? D : 0);
-    if (a.z) load_row<T, V, NV>(z, static_cast<const T*>(a.z) + at, t, tpr, D);
+    if constexpr (kStaged<NV, V>) {
+      copies_wait<kStages>();
+      rr.take(r, stage);
+      rd.take(dy, stage);
+      rx.take(x, stage);
+      if (a.dr_out) {
+        rg.take(dr, stage);
+      } else {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) dr[j] = Vec<TR, V>{};
+      }
+      if (a.z) rz.take(z, stage);
+      fetch(stage == 0 ? kStages - 1 : stage - 1, row + (kStages - 1) * stride);
+      stage = stage == kStages - 1 ? 0 : stage + 1;
+    } else {
+      load_row<TR, V, NV>(r, static_cast<const TR*>(a.r) + at, t, tpr, D);
+      load_row<T, V, NV>(dy, static_cast<const T*>(a.dy) + at, t, tpr, D);
+      load_row<T, V, NV>(x, static_cast<const T*>(a.x) + at, t, tpr, D);
+      load_row<TR, V, NV>(dr, static_cast<const TR*>(a.dr_out) + at, t, tpr, a.dr_out ? D : 0);
+      if (a.z) load_row<T, V, NV>(z, static_cast<const T*>(a.z) + at, t, tpr, D);
+    }
     float s[3] = {0.f, 0.f, 0.f};
 #pragma unroll
     for (int j = 0; j < NV; ++j)
@@ -116,8 +192,8 @@ __global__ void __launch_bounds__(TPR ? kNormThreads : kNormMaxThreads)
         s[2] = fmaf(xe, xe, s[2]);
       }
     row_sum<TPR, 3>(s, buf3, turn3);
-    const float rr = rsqrtf(fmaf(s[0], inv, a.eps));
-    const float c = s[1] * inv * rr * rr;
+    const float rs = rsqrtf(fmaf(s[0], inv, a.eps));
+    const float c = s[1] * inv * rs * rs;
     const float rx = a.w_post ? rsqrtf(fmaf(s[2], inv, a.eps)) : 1.f;
     float q[NV][V], v[NV][V], dz[NV][V], m[1] = {0.f};
 #pragma unroll
@@ -125,8 +201,8 @@ __global__ void __launch_bounds__(TPR ? kNormThreads : kNormMaxThreads)
 #pragma unroll
       for (int e = 0; e < V; ++e) {
         const float re = to_f(r[j].v[e]), d = to_f(dy[j].v[e]);
-        q[j][e] = fmaf(rr, fmaf(-c, re, d * w[j][e]), to_f(dr[j].v[e]));
-        dw[j][e] = fmaf(d, re * rr, dw[j][e]);
+        q[j][e] = fmaf(rs, fmaf(-c, re, d * w[j][e]), to_f(dr[j].v[e]));
+        dw[j][e] = fmaf(d, re * rs, dw[j][e]);
         const float xh = to_f(x[j].v[e]) * rx, u = xh * wp[j][e];
         float av = 1.f, da = 0.f;
         if (a.z) gate_slope(a.act, to_f(z[j].v[e]), &av, &da);
@@ -173,6 +249,8 @@ __global__ void __launch_bounds__(256)
   }
 }
 
+constexpr long long kForwardCtas = 2;  // per SM
+
 template <typename T, typename TR>
 struct Forward {
   const ResidualNormArgs& a;
@@ -182,8 +260,12 @@ struct Forward {
   int run() {
     const int threads = norm_threads<TPR, NV, V>(a.D), per = TPR ? kNormThreads / TPR : 1;
     const long long groups = (a.rows + per - 1) / per;
-    const int grid = int(groups < 8LL * sms ? groups : 8LL * sms);
-    residual_norm_kernel<TPR, NV, V, T, TR><<<grid, threads, 0, stream>>>(a);
+    const int grid = int(groups < kForwardCtas * sms ? groups : kForwardCtas * sms);
+    constexpr size_t kBytes = 2 * sizeof(T) + sizeof(TR);  // staged of a channel
+    constexpr size_t kThread = kStaged<NV, V> ? stages(kBytes) * NV * V * kBytes : 0;
+    constexpr int kMost = TPR ? kNormThreads : kNormMaxThreads;
+    if (!raise_smem<&residual_norm_kernel<TPR, NV, V, T, TR>>(kThread * kMost)) return GDN_ERR_LAUNCH;
+    residual_norm_kernel<TPR, NV, V, T, TR><<<grid, threads, kThread * threads, stream>>>(a);
     return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_LAUNCH;
   }
 };
@@ -199,7 +281,11 @@ struct Backward {
     const long long groups = (a.rows + per - 1) / per;
     const int most = norm_max_parts(a.rows, a.D);
     const int grid = int(groups < most ? groups : most);
-    residual_norm_backward_kernel<TPR, NV, V, T, TR><<<grid, threads, 0, stream>>>(a);
+    constexpr size_t kBytes = 3 * sizeof(T) + 2 * sizeof(TR);  // staged of a channel
+    constexpr size_t kThread = kStaged<NV, V> ? stages(kBytes) * NV * V * kBytes : 0;
+    constexpr int kMost = TPR ? kNormThreads : kNormMaxThreads;
+    if (!raise_smem<&residual_norm_backward_kernel<TPR, NV, V, T, TR>>(kThread * kMost)) return GDN_ERR_LAUNCH;
+    residual_norm_backward_kernel<TPR, NV, V, T, TR><<<grid, threads, kThread * threads, stream>>>(a);
     if (cudaGetLastError() != cudaSuccess) return GDN_ERR_LAUNCH;
     float* dst[3] = {a.dw, a.w_post ? a.dw_post : a.dscale, a.dscale};
     return launch_reduce_parts(a.part, grid, a.D * a.weights, dst, a.D, stream);

@@ -250,14 +250,6 @@ struct Stage {
 template <typename T, int V>
 constexpr bool kAsync = sizeof(T) * V >= 4;
 
-template <typename E>
-__device__ __forceinline__ void copy_async(E* dst, const E* src, int bytes) {
-  const unsigned d = static_cast<unsigned>(__cvta_generic_to_shared(dst));
-  // bytes behind `bytes` (0 or all) are zeros
-  asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(d), "l"(src),
-               "n"(sizeof(E)), "r"(bytes)
-               : "memory");
-}
 __device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // Starts the copies of tokens 0 .. cnt - 1 of a slice at p; zeros behind them.

@@ -82,6 +82,16 @@ template <typename T, int V>
 __device__ __forceinline__ Vec<T, V> load(const T* p) {
   return *reinterpret_cast<const Vec<T, V>*>(p);
 }
+// Starts an asynchronous copy of one E (4, 8 or 16 bytes) to shared memory, or
+// zeros it (bytes 0; nothing is read then).
+template <typename E>
+__device__ __forceinline__ void copy_async(E* dst, const E* src, int bytes) {
+  const unsigned d = static_cast<unsigned>(__cvta_generic_to_shared(dst));
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(d), "l"(src),
+               "n"(sizeof(E)), "r"(bytes)
+               : "memory");
+}
+
 template <typename T, int V>
 __device__ __forceinline__ void store(T* p, const float (&x)[V]) {
   Vec<T, V> r;
