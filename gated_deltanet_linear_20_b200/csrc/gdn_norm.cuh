@@ -1,193 +1,256 @@
 // What the norm kernels share: the layout of a row over threads, its sums, the
-// gate, and the choice of a layout.
+// gate, and the copies of the next rows.
 //
-// A row of D channels is held in registers by `threads per row` threads, NV
-// vectors of V channels each (vector j of thread t: channels (j TPR + t) V ..),
-// so it is read from memory once, whatever is summed over it.  Sub-warp rows
-// (TPR 8, 16, 32) share a CTA and sum by shuffles; longer ones have a CTA.
+// A row of D channels is held in registers by TPR threads, NV vectors of V
+// channels each (vector j of thread t: channels (j TPR + t) V ..), so it is read
+// from memory once, whatever is summed over it.  Short rows (TPR 8, 16, 32)
+// share a CTA of TH threads and sum by shuffles; longer ones have a CTA
+// (TPR == TH).
 //
 // CTAs are persistent, and each thread copies its part of the next rows to shared
-// memory asynchronously (a ring of two or three stages) while it works on the present one:
-// the sums over a row and their barriers would leave the memory idle otherwise.
-// A thread reads only what it copied, so the ring needs no barrier.
+// memory asynchronously (a ring of two or three stages) while it works on the
+// present one: the sums over a row and their barriers would leave the memory
+// idle otherwise.  A thread reads only what it copied, so the ring needs no
+// barrier.  What is left is the instruction count, so that all sizes of a layout
+// are constants and channels are worked on in pairs.
 #pragma once
 
 #include <algorithm>
 
+#include "gdn_host.h"
 #include "gdn_internal.h"
 #include "gdn_vec.cuh"
 
 namespace gdn {
 
-constexpr int kNormThreads = 256;     // of a CTA of sub-warp rows
-constexpr int kNormMaxThreads = 512;  // of a CTA with one row
+template <int TPR_, int TH_, int NV_, int V_>
+struct Layout {
+  static constexpr int TPR = TPR_, TH = TH_, NV = NV_, V = V_;
+  static constexpr bool kShort = TPR <= 32;   // several rows a CTA
+  static constexpr int kRows = TH / TPR;
+  static constexpr int P = V >= 2 ? 2 : 1;    // channels worked on together
+  static constexpr int N = NV * V / P;        // such groups of a thread
+  // cp.async moves at least 4 bytes, and longer rows would not fit the ring
+  static constexpr bool kStaged = V == 4 && NV * TH <= 1024;
+};
 
-// Sums of K values over the threads of a row; every thread gets them.  TPR == 0:
-// the row is the whole CTA's.  `buf` holds two sets, used in turn, so that one
-// barrier a sum is enough; the order of the additions is fixed.
-template <int TPR, int K>
-__device__ __forceinline__ void row_sum(float (&v)[K], float (*buf)[K][16], int& turn) {
-  constexpr int W = TPR == 0 ? 32 : TPR;
+// Stages of a ring whose arrays have `bytes` a channel in all: three, if the
+// longest staged row leaves room for them.
+constexpr int stages(size_t bytes) { return bytes * 4096 * 3 <= 220 * 1024 ? 3 : 2; }
+template <typename L>
+constexpr size_t ring_bytes(size_t bytes) {
+  return L::kStaged ? stages(bytes) * bytes * L::TH * L::NV * L::V : 0;
+}
+
+// This thread's place: the channel of its vector j is t V + j TPR V.
+template <typename L>
+struct Place {
+  int sub, c0, D;  // its row among the CTA's, its first channel
+  __device__ __forceinline__ explicit Place(int d)
+      : sub(L::kShort ? threadIdx.x / L::TPR : 0), c0((threadIdx.x % L::TPR) * L::V), D(d) {}
+  __device__ __forceinline__ bool has(int j) const { return c0 + j * L::TPR * L::V < D; }
+};
+
+// The channels of vector j among a thread's groups.
+template <typename L, typename T>
+__device__ __forceinline__ void spread(F<L::P> (&r)[L::N], const Vec<T, L::V>& x, int j) {
+#pragma unroll
+  for (int e = 0; e < L::V; ++e) r[(j * L::V + e) / L::P].v[e % L::P] = to_f(x.v[e]);
+}
+
+// One input array in the ring: BEFORE bytes a channel of other arrays lie before
+// it in a stage of ALL bytes a channel.
+template <typename L, typename T, int BEFORE, int ALL>
+struct Ring {
+  using E = Vec<T, L::V>;
+  static constexpr int kCh = L::TH * L::NV * L::V;
+  __device__ __forceinline__ static E* slot(unsigned char* smem, int stage, int j) {
+    return reinterpret_cast<E*>(smem + stage * (ALL * kCh) + BEFORE * kCh) + j * L::TH +
+           threadIdx.x;
+  }
+  // Channels past D stay zero in every stage.
+  __device__ __forceinline__ static void clear(unsigned char* smem, const Place<L>& at) {
+#pragma unroll
+    for (int s = 0; s < stages(ALL); ++s)
+#pragma unroll
+      for (int j = 0; j < L::NV; ++j)
+        if (!at.has(j)) *slot(smem, s, j) = E{};
+  }
+  // p: this thread's first channel of the row; a row past the end is zeros
+  __device__ __forceinline__ static void fetch(unsigned char* smem, int stage, const T* p,
+                                               const Place<L>& at, bool on) {
+#pragma unroll
+    for (int j = 0; j < L::NV; ++j)
+      if (at.has(j)) {
+        const E* src = reinterpret_cast<const E*>(p + j * L::TPR * L::V);
+        if (L::kShort)
+          copy_async(slot(smem, stage, j), src, on ? int(sizeof(E)) : 0);
+        else
+          copy_async(slot(smem, stage, j), src);
+      }
+  }
+  __device__ __forceinline__ static void take(F<L::P> (&r)[L::N], unsigned char* smem, int stage) {
+#pragma unroll
+    for (int j = 0; j < L::NV; ++j) spread<L, T>(r, *slot(smem, stage, j), j);
+  }
+};
+
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int STAGES>
+__device__ __forceinline__ void copies_wait() {  // for the oldest stage in flight
+  asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
+}
+
+// A row straight from memory (layouts that are not staged).
+template <typename L, typename T>
+__device__ __forceinline__ void load_row(F<L::P> (&r)[L::N], const T* p, const Place<L>& at,
+                                         bool on) {
+#pragma unroll
+  for (int j = 0; j < L::NV; ++j) {
+    Vec<T, L::V> x{};
+    if (on && at.has(j)) x = load<T, L::V>(p + j * L::TPR * L::V);
+    spread<L, T>(r, x, j);
+  }
+}
+
+template <typename L, typename T>
+__device__ __forceinline__ void store_row(T* p, const F<L::P> (&r)[L::N], const Place<L>& at,
+                                          bool on) {
+#pragma unroll
+  for (int j = 0; j < L::NV; ++j)
+    if (on && at.has(j)) {
+      float x[L::V];
+#pragma unroll
+      for (int e = 0; e < L::V; ++e) x[e] = r[(j * L::V + e) / L::P].v[e % L::P];
+      store<T, L::V>(p + j * L::TPR * L::V, x);
+    }
+}
+
+// The weights of this thread's channels, `offset` added; ones without any.
+template <typename L>
+__device__ __forceinline__ void load_weight(F<L::P> (&w)[L::N], const float* p, float offset,
+                                            const Place<L>& at) {
+  if (!p) {
+#pragma unroll
+    for (int i = 0; i < L::N; ++i) w[i] = all<L::P>(1.f);
+    return;
+  }
+  load_row<L, float>(w, p + at.c0, at, true);
+#pragma unroll
+  for (int i = 0; i < L::N; ++i) w[i] = add(w[i], all<L::P>(offset));
+}
+
+template <int P>
+__device__ __forceinline__ float total(F<P> a) {
+  return P == 2 ? a.v[0] + a.v[P - 1] : a.v[0];
+}
+
+// Sums of K values over the threads of a row; every thread gets them.  For rows
+// of several warps `buf` holds two sets, used in turn, so that one barrier a sum
+// is enough.  The order of the additions is fixed.
+template <typename L, int K>
+struct SumBuffer {
+  static constexpr int kWarps = L::TH / 32;
+  alignas(16) float part[2][K][kWarps < 4 ? 4 : kWarps];
+};
+template <typename L, int K>
+__device__ __forceinline__ void row_sum(float (&v)[K], SumBuffer<L, K>& buf, int& turn) {
+  constexpr int W = L::kShort ? L::TPR : 32;
 #pragma unroll
   for (int o = W / 2; o > 0; o >>= 1)
 #pragma unroll
     for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
-  if constexpr (TPR == 0) {
-    const int w = threadIdx.x >> 5, n = blockDim.x >> 5;
+  if constexpr (!L::kShort) {
+    constexpr int n = L::TH / 32;
+    static_assert(n % 4 == 0, "partial sums are read four at a time");
     if ((threadIdx.x & 31) == 0)
 #pragma unroll
-      for (int k = 0; k < K; ++k) buf[turn][k][w] = v[k];
+      for (int k = 0; k < K; ++k) buf.part[turn][k][threadIdx.x >> 5] = v[k];
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      v[k] = 0.f;
-      for (int i = 0; i < n; ++i) v[k] += buf[turn][k][i];
+      F<2> s = all<2>(0.f);
+#pragma unroll
+      for (int i = 0; i < n; i += 4) {
+        const Vec<float, 4> x = load<float, 4>(&buf.part[turn][k][i]);
+        s = add(s, add(F<2>{{x.v[0], x.v[1]}}, F<2>{{x.v[2], x.v[3]}}));
+      }
+      v[k] = total(s);
     }
     turn ^= 1;
   }
 }
 
-// The gate's value and slope.  1 / (1 + exp(-z)) from the approximate exponential
-// and quotient: a few units in the last place of fp32.
-__device__ __forceinline__ float sigmoid(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
-__device__ __forceinline__ float gate(int act, float z) {
-  const float p = sigmoid(z);
-  return act == GDN_GATE_SILU ? z * p : p;
+// 1 / (1 + exp(-z)) from the approximate power and reciprocal: a few units in
+// the last place of fp32; an overflowing exponential gives 0.
+__device__ __forceinline__ float sigmoid(float z) {
+  float e, p;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(p) : "f"(1.f + e));
+  return p;
 }
-__device__ __forceinline__ void gate_slope(int act, float z, float* a, float* da) {
-  const float p = sigmoid(z);
-  *a = act == GDN_GATE_SILU ? z * p : p;
-  *da = act == GDN_GATE_SILU ? p * (1.f + z * (1.f - p)) : p * (1.f - p);
+// The gate's value and slope.
+template <int P>
+__device__ __forceinline__ F<P> gate(int act, F<P> z) {
+  F<P> p;
+#pragma unroll
+  for (int e = 0; e < P; ++e) p.v[e] = sigmoid(z.v[e]);
+  return act == GDN_GATE_SILU ? mul(z, p) : p;
 }
-
-// Stages of a ring whose arrays have `bytes` a channel in all: three, if the
-// longest staged row leaves room for them.
-constexpr int stages(size_t bytes) { return bytes * 8 * kNormMaxThreads * 3 <= 220 * 1024 ? 3 : 2; }
-// Staged layouts: vectors of four (cp.async moves at least 4 bytes), up to two a
-// thread (larger rows would not fit the ring).
-template <int NV, int V>
-constexpr bool kStaged = V == 4 && NV <= 2;
-
-// The ring of one array: NV vectors of each thread in each stage.
-template <typename T, int V, int NV, int kStages>
-struct Ring {
-  Vec<T, V>* at;
-  __device__ __forceinline__ Ring(unsigned char*& smem) : at(reinterpret_cast<Vec<T, V>*>(smem)) {
-    smem += sizeof(Vec<T, V>) * NV * kStages * blockDim.x;
-  }
-  __device__ __forceinline__ Vec<T, V>* slot(int stage, int j) const {
-    return at + (stage * NV + j) * blockDim.x + threadIdx.x;
-  }
-  // channels c >= D are zeros (D = 0: all of them, nothing is read)
-  __device__ __forceinline__ void fetch(int stage, const T* p, int t, int tpr, int D) const {
+template <int P>
+__device__ __forceinline__ void gate_slope(int act, F<P> z, F<P>* a, F<P>* da) {
+  F<P> p;
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int c = (j * tpr + t) * V;
-      copy_async(slot(stage, j), reinterpret_cast<const Vec<T, V>*>(c < D ? p + c : p),
-                 c < D ? int(sizeof(Vec<T, V>)) : 0);
-    }
-  }
-  __device__ __forceinline__ void take(Vec<T, V> (&r)[NV], int stage) const {
-#pragma unroll
-    for (int j = 0; j < NV; ++j) r[j] = *slot(stage, j);
-  }
-};
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int kStages>
-__device__ __forceinline__ void copies_wait() {  // for the oldest stage in flight
-  asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+  for (int e = 0; e < P; ++e) p.v[e] = sigmoid(z.v[e]);
+  const F<P> one = all<P>(1.f), q = fma(p, all<P>(-1.f), one);
+  *a = act == GDN_GATE_SILU ? mul(z, p) : p;
+  *da = mul(p, act == GDN_GATE_SILU ? fma(z, q, one) : q);
 }
 
-template <typename T, int V, int NV>
-__device__ __forceinline__ void load_row(Vec<T, V> (&r)[NV], const T* p, int t, int tpr, int D) {
-#pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int c = (j * tpr + t) * V;
-    if (c < D) {
-      r[j] = load<T, V>(p + c);
-    } else {
-#pragma unroll
-      for (int e = 0; e < V; ++e) r[j].v[e] = from_f<T>(0.f);
-    }
-  }
-}
-
-// The weights of this thread's channels, `offset` added; `fill` without any.
-template <int V, int NV>
-__device__ __forceinline__ void load_weight(float (&w)[NV][V], const float* p, float offset,
-                                            float fill, int t, int tpr, int D) {
-#pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int c = (j * tpr + t) * V;
-    if (p && c < D) {
-      const Vec<float, V> v = load<float, V>(p + c);
-#pragma unroll
-      for (int e = 0; e < V; ++e) w[j][e] = v.v[e] + offset;
-    } else {
-#pragma unroll
-      for (int e = 0; e < V; ++e) w[j][e] = p ? 0.f : fill;
-    }
-  }
-}
-
-template <typename T, int V, int NV>
-__device__ __forceinline__ void store_row(T* p, const float (&x)[NV][V], int t, int tpr, int D) {
-#pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int c = (j * tpr + t) * V;
-    if (c < D) store<T, V>(p + c, x[j]);
-  }
-}
-
-// A CTA's partial sums of one weight gradient, one row of D values: the CTA's
-// rows_per_cta groups are added in order through shared memory.
-template <int TPR, int V, int NV>
-__device__ __forceinline__ void store_partial(float* part, const float (&acc)[NV][V], float* smem,
-                                              int t, int tpr, int D) {
-  if constexpr (TPR == 0) {
-    store_row<float, V, NV>(part, acc, t, tpr, D);
+// A CTA's partial sums of one weight gradient, one row of D values: its rows'
+// groups of threads are added in order through shared memory.
+template <typename L>
+__device__ __forceinline__ void store_partial(float* part, const F<L::P> (&acc)[L::N], float* smem,
+                                              const Place<L>& at) {
+  if constexpr (L::kRows == 1) {
+    store_row<L, float>(part + at.c0, acc, at, true);
   } else {
-    const int group = threadIdx.x / TPR, groups = kNormThreads / TPR;
+    constexpr int kRow = L::TPR * L::NV * L::V;
     __syncthreads();
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
+    for (int i = 0; i < L::N; ++i)
 #pragma unroll
-      for (int e = 0; e < V; ++e)
-        smem[group * (TPR * NV * V) + (j * TPR + t) * V + e] = acc[j][e];
+      for (int e = 0; e < L::P; ++e) {
+        const int k = i * L::P + e;
+        smem[at.sub * kRow + at.c0 + (k / L::V) * L::TPR * L::V + k % L::V] = acc[i].v[e];
+      }
     __syncthreads();
-    for (int c = threadIdx.x; c < D; c += kNormThreads) {
+    for (int c = threadIdx.x; c < at.D; c += L::TH) {
       float s = 0.f;
-      for (int i = 0; i < groups; ++i) s += smem[i * (TPR * NV * V) + c];
+      for (int i = 0; i < L::kRows; ++i) s += smem[i * kRow + c];
       part[c] = s;
     }
   }
 }
 
-// Calls f.template run<TPR, NV, V>() with the layout for rows of D channels:
-// vectors of four where D is a multiple of 4 and every array starts on one
-// (`wide`: 8 bytes of bf16, 16 of fp32), else single elements.  TPR 0: one CTA a
-// row.
+// Calls f.template run<Layout>() with the layout for rows of D channels: vectors
+// of four where D is a multiple of 4 and every array starts on one (`wide`: 8
+// bytes of bf16, 16 of fp32), else single elements.
 template <typename F>
 int with_layout(int D, bool wide, F&& f) {
   if (wide && D % 4 == 0) {
-    if (D <= 64) return f.template run<8, 2, 4>();
-    if (D <= 128) return f.template run<16, 2, 4>();
-    if (D <= 256) return f.template run<32, 2, 4>();
-    if (D <= 8 * kNormMaxThreads) return f.template run<0, 2, 4>();
-    if (D <= 16 * kNormMaxThreads) return f.template run<0, 4, 4>();
-    return f.template run<0, 8, 4>();
+    if (D <= 64) return f.template run<Layout<8, 256, 2, 4>>();
+    if (D <= 128) return f.template run<Layout<16, 256, 2, 4>>();
+    if (D <= 256) return f.template run<Layout<32, 256, 2, 4>>();
+    if (D <= 1024) return f.template run<Layout<128, 128, 2, 4>>();
+    if (D <= 2048) return f.template run<Layout<256, 256, 2, 4>>();
+    if (D <= 4096) return f.template run4096();
+    if (D <= 8192) return f.template run<Layout<512, 512, 4, 4>>();
+    return f.template run<Layout<512, 512, 8, 4>>();
   }
-  if (D <= 256) return f.template run<32, 8, 1>();
-  if (D <= 8 * kNormMaxThreads) return f.template run<0, 8, 1>();
-  return f.template run<0, 32, 1>();
-}
-
-// Threads of a CTA in the layout <TPR, NV, V>.
-template <int TPR, int NV, int V>
-int norm_threads(int D) {
-  if (TPR > 0) return kNormThreads;
-  const int need = (D + NV * V - 1) / (NV * V);
-  return (need + 31) / 32 * 32;
+  if (D <= 256) return f.template run<Layout<32, 256, 8, 1>>();
+  if (D <= 2048) return f.template run<Layout<256, 256, 8, 1>>();
+  return f.template run<Layout<512, 512, 32, 1>>();
 }
 
 // dst[i] = sum over parts p < n of part[p][i], i < cols.

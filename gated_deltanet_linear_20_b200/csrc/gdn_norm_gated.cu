@@ -9,190 +9,173 @@
 // directions.  The backward pass finds rstd and mean(u xh) in one sum over the
 // row (sum x^2 and sum u x), and keeps dw in registers while a CTA walks its
 // rows; the CTAs' partial sums are added by a second launch in a fixed order.
-#include "gdn_host.h"
 #include "gdn_norm.cuh"
 
 namespace gdn {
 namespace {
 
-template <int TPR, int NV, int V, typename TX, typename T>
-__global__ void __launch_bounds__(TPR ? kNormThreads : kNormMaxThreads)
-    gated_norm_kernel(const GatedNormArgs a) {
-  __shared__ float buf[2][1][16];
-  int turn = 0;
-  const int tpr = TPR ? TPR : blockDim.x, t = threadIdx.x % tpr;
-  const int per = TPR ? kNormThreads / TPR : 1;
-  float w[NV][V];
-  load_weight<V, NV>(w, a.w, a.offset, 1.f, t, tpr, a.D);
-  const float inv = 1.f / float(a.D);
-  constexpr int kStages = stages(sizeof(TX) + sizeof(T));
+template <typename L, typename TX, typename T>
+__global__ void __launch_bounds__(L::TH) gated_norm_kernel(const GatedNormArgs a) {
+  constexpr int kAll = sizeof(TX) + sizeof(T), kStages = stages(kAll), P = L::P, N = L::N;
+  using RX = Ring<L, TX, 0, kAll>;
+  using RZ = Ring<L, T, sizeof(TX), kAll>;
   extern __shared__ __align__(16) unsigned char smem[];
-  [[maybe_unused]] unsigned char* top = smem;
-  [[maybe_unused]] const Ring<TX, V, NV, kStages> rx(top);
-  [[maybe_unused]] const Ring<T, V, NV, kStages> rz(top);
-  const long long stride = (long long)gridDim.x * per;
-  const int sub = threadIdx.x / tpr;
-  const auto fetch = [&](int stage, long long row) {
-    if constexpr (kStaged<NV, V>) {
-      if (row < a.rows + per) {  // (a whole CTA's rows past the end: nothing to copy)
-        const int D = row < a.rows ? a.D : 0;
-        const size_t at = size_t(row < a.rows ? row : 0) * a.D;
-        rx.fetch(stage, static_cast<const TX*>(a.x) + at, t, tpr, D);
-        if (a.z) rz.fetch(stage, static_cast<const T*>(a.z) + at, t, tpr, D);
-      }
-      copies_commit();
+  __shared__ SumBuffer<L, 1> buf;
+  const Place<L> at(a.D);
+  const long long stride = (long long)gridDim.x * L::kRows;
+  long long row = (long long)blockIdx.x * L::kRows + at.sub, next = row;
+  int stage = 0, turn = 0, to = 0;
+  // copies row `next` to stage `to` and steps both
+  const auto fetch = [&] {
+    if (next - at.sub < a.rows) {
+      const bool on = next < a.rows;
+      const size_t o = size_t(on ? next : 0) * a.D + at.c0;
+      RX::fetch(smem, to, static_cast<const TX*>(a.x) + o, at, on);
+      if (a.z) RZ::fetch(smem, to, static_cast<const T*>(a.z) + o, at, on);
     }
+    copies_commit();
+    next += stride;
+    to = to == kStages - 1 ? 0 : to + 1;
   };
-  const long long first = (long long)blockIdx.x * per;
+  if constexpr (L::kStaged) {
+    RX::clear(smem, at);
+    RZ::clear(smem, at);
 #pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) fetch(i, first + i * stride + sub);
-  int stage = 0;
-  for (long long row0 = first; row0 < a.rows; row0 += stride) {
-    const long long row = row0 + sub;
-    const bool on = row < a.rows;
-    const size_t at = size_t(on ? row : 0) * a.D;
-    const int D = on ? a.D : 0;
-    Vec<TX, V> x[NV];
-    Vec<T, V> z[NV];
-    if constexpr (kStaged<NV, V>) {
+    for (int i = 0; i < kStages - 1; ++i) fetch();
+  }
+  F<P> w[N];
+  load_weight<L>(w, a.w, a.offset, at);
+  const float inv = 1.f / float(a.D);
+  for (; row - at.sub < a.rows; row += stride) {
+    const bool on = !L::kShort || row < a.rows;
+    const size_t o = size_t(on ? row : 0) * a.D + at.c0;
+    F<P> x[N], z[N];
+    if constexpr (L::kStaged) {
       copies_wait<kStages>();
-      rx.take(x, stage);
-      if (a.z) rz.take(z, stage);
-      fetch(stage == 0 ? kStages - 1 : stage - 1, row + (kStages - 1) * stride);
+      RX::take(x, smem, stage);
+      if (a.z) RZ::take(z, smem, stage);
       stage = stage == kStages - 1 ? 0 : stage + 1;
+      fetch();
     } else {
-      load_row<TX, V, NV>(x, static_cast<const TX*>(a.x) + at, t, tpr, D);
-      if (a.z) load_row<T, V, NV>(z, static_cast<const T*>(a.z) + at, t, tpr, D);
+      load_row<L, TX>(x, static_cast<const TX*>(a.x) + o, at, on);
+      if (a.z) load_row<L, T>(z, static_cast<const T*>(a.z) + o, at, on);
     }
-    float s[1] = {0.f};
+    F<P> sq = all<P>(0.f);
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
+    for (int i = 0; i < N; ++i) sq = fma(x[i], x[i], sq);
+    float s[1] = {total(sq)};
+    row_sum<L, 1>(s, buf, turn);
+    const F<P> rstd = all<P>(rsqrtf(fmaf(s[0], inv, a.eps)));
 #pragma unroll
-      for (int e = 0; e < V; ++e) s[0] = fmaf(to_f(x[j].v[e]), to_f(x[j].v[e]), s[0]);
-    row_sum<TPR, 1>(s, buf, turn);
-    const float rstd = rsqrtf(fmaf(s[0], inv, a.eps));
-    float y[NV][V];
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        y[j][e] = to_f(x[j].v[e]) * rstd * w[j][e];
-        if (a.z) y[j][e] *= gate(a.act, to_f(z[j].v[e]));
-      }
-    store_row<T, V, NV>(static_cast<T*>(a.y) + at, y, t, tpr, D);
+    for (int i = 0; i < N; ++i) {
+      x[i] = mul(mul(x[i], rstd), w[i]);
+      if (a.z) x[i] = mul(x[i], gate(a.act, z[i]));
+    }
+    store_row<L, T>(static_cast<T*>(a.y) + o, x, at, on);
   }
 }
 
-template <int TPR, int NV, int V, typename TX, typename T>
-__global__ void __launch_bounds__(TPR ? kNormThreads : kNormMaxThreads)
-    gated_norm_backward_kernel(const GatedNormArgs a) {
-  __shared__ float buf[2][2][16];
-  __shared__ float groups[TPR ? kNormThreads * NV * V : 1];
-  int turn = 0;
-  const int tpr = TPR ? TPR : blockDim.x, t = threadIdx.x % tpr;
-  const int per = TPR ? kNormThreads / TPR : 1;
-  float w[NV][V], dw[NV][V];
-  load_weight<V, NV>(w, a.w, a.offset, 1.f, t, tpr, a.D);
-#pragma unroll
-  for (int j = 0; j < NV; ++j)
-#pragma unroll
-    for (int e = 0; e < V; ++e) dw[j][e] = 0.f;
-  const float inv = 1.f / float(a.D);
-  constexpr int kStages = stages(sizeof(TX) + 2 * sizeof(T));
+template <typename L, typename TX, typename T>
+__global__ void __launch_bounds__(L::TH) gated_norm_backward_kernel(const GatedNormArgs a) {
+  constexpr int kAll = sizeof(TX) + 2 * sizeof(T), kStages = stages(kAll), P = L::P, N = L::N;
+  using RX = Ring<L, TX, 0, kAll>;
+  using RD = Ring<L, T, sizeof(TX), kAll>;
+  using RZ = Ring<L, T, sizeof(TX) + sizeof(T), kAll>;
   extern __shared__ __align__(16) unsigned char smem[];
-  [[maybe_unused]] unsigned char* top = smem;
-  [[maybe_unused]] const Ring<TX, V, NV, kStages> rx(top);
-  [[maybe_unused]] const Ring<T, V, NV, kStages> rd(top);
-  [[maybe_unused]] const Ring<T, V, NV, kStages> rz(top);
-  const long long stride = (long long)gridDim.x * per;
-  const int sub = threadIdx.x / tpr;
-  const auto fetch = [&](int stage, long long row) {
-    if constexpr (kStaged<NV, V>) {
-      if (row < a.rows + per) {  // (a whole CTA's rows past the end: nothing to copy)
-        const int D = row < a.rows ? a.D : 0;
-        const size_t at = size_t(row < a.rows ? row : 0) * a.D;
-        rx.fetch(stage, static_cast<const TX*>(a.x) + at, t, tpr, D);
-        rd.fetch(stage, static_cast<const T*>(a.dy) + at, t, tpr, D);
-        if (a.z) rz.fetch(stage, static_cast<const T*>(a.z) + at, t, tpr, D);
-      }
-      copies_commit();
+  __shared__ SumBuffer<L, 2> buf;
+  __shared__ float groups[L::kShort ? L::TH * L::NV * L::V : 1];
+  const Place<L> at(a.D);
+  const long long stride = (long long)gridDim.x * L::kRows;
+  long long row = (long long)blockIdx.x * L::kRows + at.sub, next = row;
+  int stage = 0, turn = 0, to = 0;
+  const auto fetch = [&] {
+    if (next - at.sub < a.rows) {
+      const bool on = next < a.rows;
+      const size_t o = size_t(on ? next : 0) * a.D + at.c0;
+      RX::fetch(smem, to, static_cast<const TX*>(a.x) + o, at, on);
+      RD::fetch(smem, to, static_cast<const T*>(a.dy) + o, at, on);
+      if (a.z) RZ::fetch(smem, to, static_cast<const T*>(a.z) + o, at, on);
     }
+    copies_commit();
+    next += stride;
+    to = to == kStages - 1 ? 0 : to + 1;
   };
-  const long long first = (long long)blockIdx.x * per;
+  if constexpr (L::kStaged) {
+    RX::clear(smem, at);
+    RD::clear(smem, at);
+    RZ::clear(smem, at);
 #pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) fetch(i, first + i * stride + sub);
-  int stage = 0;
-  for (long long row0 = first; row0 < a.rows; row0 += stride) {
-    const long long row = row0 + sub;
-    const bool on = row < a.rows;
-    const size_t at = size_t(on ? row : 0) * a.D;
-    const int D = on ? a.D : 0;
-    Vec<TX, V> x[NV];
-    Vec<T, V> z[NV], dy[NV];
-    if constexpr (kStaged<NV, V>) {
-      copies_wait<kStages>();
-      rx.take(x, stage);
-      rd.take(dy, stage);
-      if (a.z) rz.take(z, stage);
-      fetch(stage == 0 ? kStages - 1 : stage - 1, row + (kStages - 1) * stride);
-      stage = stage == kStages - 1 ? 0 : stage + 1;
-    } else {
-      load_row<TX, V, NV>(x, static_cast<const TX*>(a.x) + at, t, tpr, D);
-      load_row<T, V, NV>(dy, static_cast<const T*>(a.dy) + at, t, tpr, D);
-      if (a.z) load_row<T, V, NV>(z, static_cast<const T*>(a.z) + at, t, tpr, D);
-    }
-    float u[NV][V], dz[NV][V], s[2] = {0.f, 0.f};
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float xe = to_f(x[j].v[e]), d = to_f(dy[j].v[e]);
-        float av = 1.f, da = 0.f;
-        if (a.z) gate_slope(a.act, to_f(z[j].v[e]), &av, &da);
-        u[j][e] = d * av;            // times w below: dw wants it without
-        dz[j][e] = d * w[j][e] * da * xe;
-        s[0] = fmaf(xe, xe, s[0]);
-        s[1] = fmaf(u[j][e] * w[j][e], xe, s[1]);
-      }
-    row_sum<TPR, 2>(s, buf, turn);
-    const float rstd = rsqrtf(fmaf(s[0], inv, a.eps));
-    const float c = s[1] * inv * rstd * rstd;  // mean(u xh) rstd
-    float dx[NV][V];
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float xe = to_f(x[j].v[e]);
-        dw[j][e] = fmaf(u[j][e], xe * rstd, dw[j][e]);
-        dx[j][e] = rstd * fmaf(-c, xe, u[j][e] * w[j][e]);
-        dz[j][e] *= rstd;
-      }
-    store_row<TX, V, NV>(static_cast<TX*>(a.dx) + at, dx, t, tpr, D);
-    if (a.z) store_row<T, V, NV>(static_cast<T*>(a.dz) + at, dz, t, tpr, D);
+    for (int i = 0; i < kStages - 1; ++i) fetch();
   }
-  if (a.part)
-    store_partial<TPR, V, NV>(a.part + size_t(blockIdx.x) * a.D, dw, groups, t, tpr, a.D);
+  F<P> w[N], dw[N];
+  load_weight<L>(w, a.w, a.offset, at);
+#pragma unroll
+  for (int i = 0; i < N; ++i) dw[i] = all<P>(0.f);
+  const float inv = 1.f / float(a.D);
+  for (; row - at.sub < a.rows; row += stride) {
+    const bool on = !L::kShort || row < a.rows;
+    const size_t o = size_t(on ? row : 0) * a.D + at.c0;
+    F<P> x[N], dy[N], z[N];
+    if constexpr (L::kStaged) {
+      copies_wait<kStages>();
+      RX::take(x, smem, stage);
+      RD::take(dy, smem, stage);
+      if (a.z) RZ::take(z, smem, stage);
+      stage = stage == kStages - 1 ? 0 : stage + 1;
+      fetch();
+    } else {
+      load_row<L, TX>(x, static_cast<const TX*>(a.x) + o, at, on);
+      load_row<L, T>(dy, static_cast<const T*>(a.dy) + o, at, on);
+      if (a.z) load_row<L, T>(z, static_cast<const T*>(a.z) + o, at, on);
+    }
+    F<P> sq = all<P>(0.f), su = all<P>(0.f);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      sq = fma(x[i], x[i], sq);
+      if (a.z) {
+        F<P> av, da;
+        gate_slope(a.act, z[i], &av, &da);
+        z[i] = mul(mul(mul(dy[i], w[i]), x[i]), da);  // dz, but for rstd
+        dy[i] = mul(dy[i], av);                       // u without w
+      }
+      su = fma(mul(dy[i], w[i]), x[i], su);
+    }
+    float s[2] = {total(sq), total(su)};
+    row_sum<L, 2>(s, buf, turn);
+    const float r = rsqrtf(fmaf(s[0], inv, a.eps));
+    const F<P> rstd = all<P>(r), c = all<P>(-(s[1] * inv * r * r));  // -mean(u xh) rstd
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      dw[i] = fma(dy[i], mul(x[i], rstd), dw[i]);
+      x[i] = mul(rstd, fma(c, x[i], mul(dy[i], w[i])));
+    }
+    store_row<L, TX>(static_cast<TX*>(a.dx) + o, x, at, on);
+    if (a.z) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) z[i] = mul(z[i], rstd);
+      store_row<L, T>(static_cast<T*>(a.dz) + o, z, at, on);
+    }
+  }
+  store_partial<L>(a.part + size_t(blockIdx.x) * a.D, dw, groups, at);
 }
 
-constexpr long long kForwardCtas = 8;  // per SM
+constexpr long long kForwardCtas = 16;  // per SM: 8 rows of a CTA at a time are resident
 
 template <typename TX, typename T>
 struct Forward {
   const GatedNormArgs& a;
   int sms;
   cudaStream_t stream;
-  template <int TPR, int NV, int V>
+  template <typename L>
   int run() {
-    const int threads = norm_threads<TPR, NV, V>(a.D), per = TPR ? kNormThreads / TPR : 1;
-    const long long groups = (a.rows + per - 1) / per;
-    const int grid = int(groups < kForwardCtas * sms ? groups : kForwardCtas * sms);
-    constexpr size_t kBytes = sizeof(TX) + sizeof(T);  // staged of a channel
-    constexpr size_t kThread = kStaged<NV, V> ? stages(kBytes) * NV * V * kBytes : 0;
-    constexpr int kMost = TPR ? kNormThreads : kNormMaxThreads;
-    if (!raise_smem<&gated_norm_kernel<TPR, NV, V, TX, T>>(kThread * kMost)) return GDN_ERR_LAUNCH;
-    gated_norm_kernel<TPR, NV, V, TX, T><<<grid, threads, kThread * threads, stream>>>(a);
+    const long long groups = (a.rows + L::kRows - 1) / L::kRows;
+    const int grid = int(std::min(groups, kForwardCtas * sms));
+    constexpr size_t smem = ring_bytes<L>(sizeof(TX) + sizeof(T));
+    if (!raise_smem<&gated_norm_kernel<L, TX, T>>(smem)) return GDN_ERR_LAUNCH;
+    gated_norm_kernel<L, TX, T><<<grid, L::TH, smem, stream>>>(a);
     return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_LAUNCH;
   }
+  int run4096() { return run<Layout<256, 256, 4, 4>>(); }
 };
 
 template <typename TX, typename T>
@@ -200,33 +183,30 @@ struct Backward {
   const GatedNormArgs& a;
   int sms;
   cudaStream_t stream;
-  template <int TPR, int NV, int V>
+  template <typename L>
   int run() {
-    const int threads = norm_threads<TPR, NV, V>(a.D), per = TPR ? kNormThreads / TPR : 1;
-    const long long groups = (a.rows + per - 1) / per;
-    const int most = norm_max_parts(a.rows, a.D);
-    const int grid = int(groups < most ? groups : most);
-    constexpr size_t kBytes = sizeof(TX) + 2 * sizeof(T);  // staged of a channel
-    constexpr size_t kThread = kStaged<NV, V> ? stages(kBytes) * NV * V * kBytes : 0;
-    constexpr int kMost = TPR ? kNormThreads : kNormMaxThreads;
-    if (!raise_smem<&gated_norm_backward_kernel<TPR, NV, V, TX, T>>(kThread * kMost)) return GDN_ERR_LAUNCH;
-    gated_norm_backward_kernel<TPR, NV, V, TX, T><<<grid, threads, kThread * threads, stream>>>(a);
+    const long long groups = (a.rows + L::kRows - 1) / L::kRows;
+    const int grid = int(std::min<long long>(groups, norm_max_parts(a.rows, a.D)));
+    constexpr size_t smem = ring_bytes<L>(sizeof(TX) + 2 * sizeof(T));
+    if (!raise_smem<&gated_norm_backward_kernel<L, TX, T>>(smem)) return GDN_ERR_LAUNCH;
+    gated_norm_backward_kernel<L, TX, T><<<grid, L::TH, smem, stream>>>(a);
     if (cudaGetLastError() != cudaSuccess) return GDN_ERR_LAUNCH;
     return launch_reduce_parts(a.part, grid, a.D, &a.dw, a.D, stream);
   }
+  int run4096() { return run<Layout<512, 512, 2, 4>>(); }
 };
 
-bool wide_ok(const GatedNormArgs& a) {
-  const void* p[] = {a.x, a.z, a.w, a.y, a.dy, a.dx, a.dz, a.part};
-  uintptr_t all = 0;
-  for (const void* q : p) all |= reinterpret_cast<uintptr_t>(q);
-  return (all & 15) == 0;
+// Whether every array starts on four elements.
+bool wide_ok(const GatedNormArgs& a, int x_dtype, int dtype) {
+  const uintptr_t ex = x_dtype == GDN_BF16 ? 8 : 16, e = dtype == GDN_BF16 ? 8 : 16;
+  return aligned(a.x, ex) && aligned(a.dx, ex) && aligned(a.z, e) && aligned(a.y, e) &&
+         aligned(a.dy, e) && aligned(a.dz, e) && aligned(a.w, 16);
 }
 
 template <template <typename, typename> class Run>
 int dispatch(const GatedNormArgs& a, int x_dtype, int dtype, int sms, cudaStream_t stream) {
   using B = __nv_bfloat16;
-  const bool wide = wide_ok(a);
+  const bool wide = wide_ok(a, x_dtype, dtype);
   if (x_dtype == GDN_BF16)
     return dtype == GDN_BF16 ? with_layout(a.D, wide, Run<B, B>{a, sms, stream})
                              : with_layout(a.D, wide, Run<B, float>{a, sms, stream});

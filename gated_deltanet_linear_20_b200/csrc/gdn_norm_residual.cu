@@ -12,225 +12,211 @@
 // only inputs in the first sum).  y comes from the fp32 sum before r' is rounded
 // to its type.  The weight gradients of a CTA's rows stay in registers and the
 // CTAs' partial sums are added by a second launch in a fixed order.
-#include "gdn_host.h"
 #include "gdn_norm.cuh"
 
 namespace gdn {
 namespace {
 
-template <int TPR, int NV, int V, typename T, typename TR>
-__global__ void __launch_bounds__(TPR ? kNormThreads : kNormMaxThreads)
-    residual_norm_kernel(const ResidualNormArgs a) {
-  __shared__ float buf[2][1][16];
-  int turn = 0;
-  const int tpr = TPR ? TPR : blockDim.x, t = threadIdx.x % tpr;
-  const int per = TPR ? kNormThreads / TPR : 1;
-  float w[NV][V], wp[NV][V], sc[NV][V];
-  load_weight<V, NV>(w, a.w, a.offset, 1.f, t, tpr, a.D);
-  load_weight<V, NV>(wp, a.w_post, a.offset, 1.f, t, tpr, a.D);
-  load_weight<V, NV>(sc, a.scale, 0.f, 1.f, t, tpr, a.D);
-#pragma unroll
-  for (int j = 0; j < NV; ++j)
-#pragma unroll
-    for (int e = 0; e < V; ++e) wp[j][e] *= sc[j][e];
-  const float inv = 1.f / float(a.D);
-  constexpr int kStages = stages(2 * sizeof(T) + sizeof(TR));
+template <typename L, typename T, typename TR>
+__global__ void __launch_bounds__(L::TH) residual_norm_kernel(const ResidualNormArgs a) {
+  constexpr int kAll = 2 * sizeof(T) + sizeof(TR), kStages = stages(kAll), P = L::P, N = L::N;
+  using RR = Ring<L, TR, 0, kAll>;
+  using RX = Ring<L, T, sizeof(TR), kAll>;
+  using RZ = Ring<L, T, sizeof(TR) + sizeof(T), kAll>;
   extern __shared__ __align__(16) unsigned char smem[];
-  [[maybe_unused]] unsigned char* top = smem;
-  [[maybe_unused]] const Ring<TR, V, NV, kStages> rr(top);
-  [[maybe_unused]] const Ring<T, V, NV, kStages> rx(top);
-  [[maybe_unused]] const Ring<T, V, NV, kStages> rz(top);
-  const long long stride = (long long)gridDim.x * per;
-  const int sub = threadIdx.x / tpr;
-  const auto fetch = [&](int stage, long long row) {
-    if constexpr (kStaged<NV, V>) {
-      if (row < a.rows + per) {  // (a whole CTA's rows past the end: nothing to copy)
-        const int D = row < a.rows ? a.D : 0;
-        const size_t at = size_t(row < a.rows ? row : 0) * a.D;
-        rx.fetch(stage, static_cast<const T*>(a.x) + at, t, tpr, D);
-        rr.fetch(stage, static_cast<const TR*>(a.r) + at, t, tpr, D);
-        if (a.z) rz.fetch(stage, static_cast<const T*>(a.z) + at, t, tpr, D);
-      }
-      copies_commit();
+  __shared__ SumBuffer<L, 1> buf;
+  const Place<L> at(a.D);
+  const long long stride = (long long)gridDim.x * L::kRows;
+  long long row = (long long)blockIdx.x * L::kRows + at.sub, next = row;
+  int stage = 0, turn = 0, to = 0;
+  // copies row `next` to stage `to` and steps both
+  const auto fetch = [&] {
+    if (next - at.sub < a.rows) {
+      const bool on = next < a.rows;
+      const size_t o = size_t(on ? next : 0) * a.D + at.c0;
+      RX::fetch(smem, to, static_cast<const T*>(a.x) + o, at, on);
+      RR::fetch(smem, to, static_cast<const TR*>(a.r) + o, at, on);
+      if (a.z) RZ::fetch(smem, to, static_cast<const T*>(a.z) + o, at, on);
     }
+    copies_commit();
+    next += stride;
+    to = to == kStages - 1 ? 0 : to + 1;
   };
-  const long long first = (long long)blockIdx.x * per;
+  if constexpr (L::kStaged) {
+    RR::clear(smem, at);
+    RX::clear(smem, at);
+    RZ::clear(smem, at);
 #pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) fetch(i, first + i * stride + sub);
-  int stage = 0;
-  for (long long row0 = first; row0 < a.rows; row0 += stride) {
-    const long long row = row0 + sub;
-    const bool on = row < a.rows;
-    const size_t at = size_t(on ? row : 0) * a.D;
-    const int D = on ? a.D : 0;
-    Vec<T, V> x[NV], z[NV];
-    Vec<TR, V> r[NV];
-    if constexpr (kStaged<NV, V>) {
+    for (int i = 0; i < kStages - 1; ++i) fetch();
+  }
+  F<P> w[N], wp[N];  // wp: the post norm's weight times the scale
+  load_weight<L>(w, a.scale, 0.f, at);
+  load_weight<L>(wp, a.w_post, a.offset, at);
+#pragma unroll
+  for (int i = 0; i < N; ++i) wp[i] = mul(wp[i], w[i]);
+  load_weight<L>(w, a.w, a.offset, at);
+  const float inv = 1.f / float(a.D);
+  for (; row - at.sub < a.rows; row += stride) {
+    const bool on = !L::kShort || row < a.rows;
+    const size_t o = size_t(on ? row : 0) * a.D + at.c0;
+    F<P> x[N], r[N], z[N];
+    if constexpr (L::kStaged) {
       copies_wait<kStages>();
-      rx.take(x, stage);
-      rr.take(r, stage);
-      if (a.z) rz.take(z, stage);
-      fetch(stage == 0 ? kStages - 1 : stage - 1, row + (kStages - 1) * stride);
+      RX::take(x, smem, stage);
+      RR::take(r, smem, stage);
+      if (a.z) RZ::take(z, smem, stage);
       stage = stage == kStages - 1 ? 0 : stage + 1;
+      fetch();
     } else {
-      load_row<T, V, NV>(x, static_cast<const T*>(a.x) + at, t, tpr, D);
-      load_row<TR, V, NV>(r, static_cast<const TR*>(a.r) + at, t, tpr, D);
-      if (a.z) load_row<T, V, NV>(z, static_cast<const T*>(a.z) + at, t, tpr, D);
+      load_row<L, T>(x, static_cast<const T*>(a.x) + o, at, on);
+      load_row<L, TR>(r, static_cast<const TR*>(a.r) + o, at, on);
+      if (a.z) load_row<L, T>(z, static_cast<const T*>(a.z) + o, at, on);
     }
     float rstd = 1.f;
     if (a.w_post) {
-      float s[1] = {0.f};
+      F<P> sq = all<P>(0.f);
 #pragma unroll
-      for (int j = 0; j < NV; ++j)
-#pragma unroll
-        for (int e = 0; e < V; ++e) s[0] = fmaf(to_f(x[j].v[e]), to_f(x[j].v[e]), s[0]);
-      row_sum<TPR, 1>(s, buf, turn);
+      for (int i = 0; i < N; ++i) sq = fma(x[i], x[i], sq);
+      float s[1] = {total(sq)};
+      row_sum<L, 1>(s, buf, turn);
       rstd = rsqrtf(fmaf(s[0], inv, a.eps));
     }
-    float q[NV][V], s[1] = {0.f};
+    F<P> sq = all<P>(0.f);
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
+    for (int i = 0; i < N; ++i) {
+      x[i] = mul(x[i], all<P>(rstd));
+      if (a.z) x[i] = mul(x[i], gate(a.act, z[i]));
+      r[i] = fma(x[i], wp[i], r[i]);
+      sq = fma(r[i], r[i], sq);
+    }
+    store_row<L, TR>(static_cast<TR*>(a.r_out) + o, r, at, on);
+    float s[1] = {total(sq)};
+    row_sum<L, 1>(s, buf, turn);
+    const F<P> rs = all<P>(rsqrtf(fmaf(s[0], inv, a.eps)));
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        float u = to_f(x[j].v[e]) * rstd * wp[j][e];
-        if (a.z) u *= gate(a.act, to_f(z[j].v[e]));
-        q[j][e] = to_f(r[j].v[e]) + u;
-        s[0] = fmaf(q[j][e], q[j][e], s[0]);
-      }
-    store_row<TR, V, NV>(static_cast<TR*>(a.r_out) + at, q, t, tpr, D);
-    row_sum<TPR, 1>(s, buf, turn);
-    const float rs = rsqrtf(fmaf(s[0], inv, a.eps));
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-      for (int e = 0; e < V; ++e) q[j][e] *= rs * w[j][e];
-    store_row<T, V, NV>(static_cast<T*>(a.y) + at, q, t, tpr, D);
+    for (int i = 0; i < N; ++i) r[i] = mul(mul(r[i], rs), w[i]);
+    store_row<L, T>(static_cast<T*>(a.y) + o, r, at, on);
   }
 }
 
-template <int TPR, int NV, int V, typename T, typename TR>
-__global__ void __launch_bounds__(TPR ? kNormThreads : kNormMaxThreads)
-    residual_norm_backward_kernel(const ResidualNormArgs a) {
-  __shared__ float buf3[2][3][16], buf1[2][1][16];
-  __shared__ float groups[TPR ? kNormThreads * NV * V : 1];
-  int turn3 = 0, turn1 = 0;
-  const int tpr = TPR ? TPR : blockDim.x, t = threadIdx.x % tpr;
-  const int per = TPR ? kNormThreads / TPR : 1;
-  float w[NV][V], wp[NV][V], sc[NV][V], dw[NV][V], dwp[NV][V], dsc[NV][V];
-  load_weight<V, NV>(w, a.w, a.offset, 1.f, t, tpr, a.D);
-  load_weight<V, NV>(wp, a.w_post, a.offset, 1.f, t, tpr, a.D);
-  load_weight<V, NV>(sc, a.scale, 0.f, 1.f, t, tpr, a.D);
-#pragma unroll
-  for (int j = 0; j < NV; ++j)
-#pragma unroll
-    for (int e = 0; e < V; ++e) dw[j][e] = dwp[j][e] = dsc[j][e] = 0.f;
-  const float inv = 1.f / float(a.D);
-  constexpr int kStages = stages(3 * sizeof(T) + 2 * sizeof(TR));
+template <typename L, typename T, typename TR>
+__global__ void __launch_bounds__(L::TH) residual_norm_backward_kernel(const ResidualNormArgs a) {
+  constexpr int kT = sizeof(T), kR = sizeof(TR), kAll = 3 * kT + 2 * kR, kStages = stages(kAll);
+  constexpr int P = L::P, N = L::N;
+  using RR = Ring<L, TR, 0, kAll>;
+  using RG = Ring<L, TR, kR, kAll>;
+  using RD = Ring<L, T, 2 * kR, kAll>;
+  using RX = Ring<L, T, 2 * kR + kT, kAll>;
+  using RZ = Ring<L, T, 2 * kR + 2 * kT, kAll>;
   extern __shared__ __align__(16) unsigned char smem[];
-  [[maybe_unused]] unsigned char* top = smem;
-  [[maybe_unused]] const Ring<TR, V, NV, kStages> rr(top);
-  [[maybe_unused]] const Ring<TR, V, NV, kStages> rg(top);
-  [[maybe_unused]] const Ring<T, V, NV, kStages> rd(top);
-  [[maybe_unused]] const Ring<T, V, NV, kStages> rx(top);
-  [[maybe_unused]] const Ring<T, V, NV, kStages> rz(top);
-  const long long stride = (long long)gridDim.x * per;
-  const int sub = threadIdx.x / tpr;
-  const auto fetch = [&](int stage, long long row) {
-    if constexpr (kStaged<NV, V>) {
-      if (row < a.rows + per) {  // (a whole CTA's rows past the end: nothing to copy)
-        const int D = row < a.rows ? a.D : 0;
-        const size_t at = size_t(row < a.rows ? row : 0) * a.D;
-        rr.fetch(stage, static_cast<const TR*>(a.r) + at, t, tpr, D);
-        rd.fetch(stage, static_cast<const T*>(a.dy) + at, t, tpr, D);
-        rx.fetch(stage, static_cast<const T*>(a.x) + at, t, tpr, D);
-        if (a.dr_out) rg.fetch(stage, static_cast<const TR*>(a.dr_out) + at, t, tpr, D);
-        if (a.z) rz.fetch(stage, static_cast<const T*>(a.z) + at, t, tpr, D);
-      }
-      copies_commit();
+  __shared__ SumBuffer<L, 3> buf3;
+  __shared__ SumBuffer<L, 1> buf1;
+  __shared__ float groups[L::kShort ? L::TH * L::NV * L::V : 1];
+  const Place<L> at(a.D);
+  const long long stride = (long long)gridDim.x * L::kRows;
+  long long row = (long long)blockIdx.x * L::kRows + at.sub, next = row;
+  int stage = 0, turn3 = 0, turn1 = 0, to = 0;
+  const auto fetch = [&] {
+    if (next - at.sub < a.rows) {
+      const bool on = next < a.rows;
+      const size_t o = size_t(on ? next : 0) * a.D + at.c0;
+      RR::fetch(smem, to, static_cast<const TR*>(a.r) + o, at, on);
+      RD::fetch(smem, to, static_cast<const T*>(a.dy) + o, at, on);
+      RX::fetch(smem, to, static_cast<const T*>(a.x) + o, at, on);
+      if (a.dr_out) RG::fetch(smem, to, static_cast<const TR*>(a.dr_out) + o, at, on);
+      if (a.z) RZ::fetch(smem, to, static_cast<const T*>(a.z) + o, at, on);
     }
+    copies_commit();
+    next += stride;
+    to = to == kStages - 1 ? 0 : to + 1;
   };
-  const long long first = (long long)blockIdx.x * per;
+  if constexpr (L::kStaged) {
+    RR::clear(smem, at);
+    RG::clear(smem, at);
+    RD::clear(smem, at);
+    RX::clear(smem, at);
+    RZ::clear(smem, at);
 #pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) fetch(i, first + i * stride + sub);
-  int stage = 0;
-  for (long long row0 = first; row0 < a.rows; row0 += stride) {
-    const long long row = row0 + sub;
-    const bool on = row < a.rows;
-    const size_t at = size_t(on ? row : 0) * a.D;
-    const int D = on ? a.D : 0;
-    Vec<T, V> x[NV], z[NV], dy[NV];
-    Vec<TR, V> r[NV], dr[NV];
-    if constexpr (kStaged<NV, V>) {
+    for (int i = 0; i < kStages - 1; ++i) fetch();
+  }
+  F<P> w[N], wp[N], sc[N], dw[N], dwp[N], dsc[N];
+  load_weight<L>(w, a.w, a.offset, at);
+  load_weight<L>(wp, a.w_post, a.offset, at);
+  load_weight<L>(sc, a.scale, 0.f, at);
+#pragma unroll
+  for (int i = 0; i < N; ++i) dw[i] = dwp[i] = dsc[i] = all<P>(0.f);
+  const float inv = 1.f / float(a.D);
+  for (; row - at.sub < a.rows; row += stride) {
+    const bool on = !L::kShort || row < a.rows;
+    const size_t o = size_t(on ? row : 0) * a.D + at.c0;
+    F<P> x[N], z[N], dy[N], r[N], q[N];
+    if constexpr (L::kStaged) {
       copies_wait<kStages>();
-      rr.take(r, stage);
-      rd.take(dy, stage);
-      rx.take(x, stage);
-      if (a.dr_out) {
-        rg.take(dr, stage);
-      } else {
-#pragma unroll
-        for (int j = 0; j < NV; ++j) dr[j] = Vec<TR, V>{};
-      }
-      if (a.z) rz.take(z, stage);
-      fetch(stage == 0 ? kStages - 1 : stage - 1, row + (kStages - 1) * stride);
+      RR::take(r, smem, stage);
+      RD::take(dy, smem, stage);
+      RX::take(x, smem, stage);
+      if (a.dr_out) RG::take(q, smem, stage);
+      if (a.z) RZ::take(z, smem, stage);
       stage = stage == kStages - 1 ? 0 : stage + 1;
+      fetch();
     } else {
-      load_row<TR, V, NV>(r, static_cast<const TR*>(a.r) + at, t, tpr, D);
-      load_row<T, V, NV>(dy, static_cast<const T*>(a.dy) + at, t, tpr, D);
-      load_row<T, V, NV>(x, static_cast<const T*>(a.x) + at, t, tpr, D);
-      load_row<TR, V, NV>(dr, static_cast<const TR*>(a.dr_out) + at, t, tpr, a.dr_out ? D : 0);
-      if (a.z) load_row<T, V, NV>(z, static_cast<const T*>(a.z) + at, t, tpr, D);
+      load_row<L, TR>(r, static_cast<const TR*>(a.r) + o, at, on);
+      load_row<L, T>(dy, static_cast<const T*>(a.dy) + o, at, on);
+      load_row<L, T>(x, static_cast<const T*>(a.x) + o, at, on);
+      if (a.dr_out) load_row<L, TR>(q, static_cast<const TR*>(a.dr_out) + o, at, on);
+      if (a.z) load_row<L, T>(z, static_cast<const T*>(a.z) + o, at, on);
     }
-    float s[3] = {0.f, 0.f, 0.f};
+    if (!a.dr_out) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
+      for (int i = 0; i < N; ++i) q[i] = all<P>(0.f);
+    }
+    F<P> s0 = all<P>(0.f), s1 = s0, s2 = s0;
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float re = to_f(r[j].v[e]), xe = to_f(x[j].v[e]);
-        s[0] = fmaf(re, re, s[0]);
-        s[1] = fmaf(to_f(dy[j].v[e]) * w[j][e], re, s[1]);
-        s[2] = fmaf(xe, xe, s[2]);
-      }
-    row_sum<TPR, 3>(s, buf3, turn3);
+    for (int i = 0; i < N; ++i) {
+      s0 = fma(r[i], r[i], s0);
+      s1 = fma(mul(dy[i], w[i]), r[i], s1);
+      s2 = fma(x[i], x[i], s2);
+    }
+    float s[3] = {total(s0), total(s1), total(s2)};
+    row_sum<L, 3>(s, buf3, turn3);
     const float rs = rsqrtf(fmaf(s[0], inv, a.eps));
-    const float c = s[1] * inv * rs * rs;
     const float rx = a.w_post ? rsqrtf(fmaf(s[2], inv, a.eps)) : 1.f;
-    float q[NV][V], v[NV][V], dz[NV][V], m[1] = {0.f};
+    const F<P> rr = all<P>(rs), c = all<P>(-(s[1] * inv * rs * rs)), rp = all<P>(rx);
+    F<P> sm = all<P>(0.f);
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float re = to_f(r[j].v[e]), d = to_f(dy[j].v[e]);
-        q[j][e] = fmaf(rs, fmaf(-c, re, d * w[j][e]), to_f(dr[j].v[e]));
-        dw[j][e] = fmaf(d, re * rs, dw[j][e]);
-        const float xh = to_f(x[j].v[e]) * rx, u = xh * wp[j][e];
-        float av = 1.f, da = 0.f;
-        if (a.z) gate_slope(a.act, to_f(z[j].v[e]), &av, &da);
-        const float qa = q[j][e] * av;
-        dsc[j][e] = fmaf(qa, u, dsc[j][e]);
-        dz[j][e] = q[j][e] * sc[j][e] * u * da;
-        v[j][e] = qa * sc[j][e];
-        dwp[j][e] = fmaf(v[j][e], xh, dwp[j][e]);
-        m[0] = fmaf(v[j][e], u, m[0]);
+    for (int i = 0; i < N; ++i) {
+      q[i] = fma(rr, fma(c, r[i], mul(dy[i], w[i])), q[i]);
+      dw[i] = fma(dy[i], mul(r[i], rr), dw[i]);
+      x[i] = mul(x[i], rp);  // xh
+      const F<P> u = mul(x[i], wp[i]);
+      F<P> qa = q[i];
+      if (a.z) {
+        F<P> av, da;
+        gate_slope(a.act, z[i], &av, &da);
+        qa = mul(qa, av);
+        z[i] = mul(mul(mul(q[i], sc[i]), u), da);  // dz
       }
-    store_row<TR, V, NV>(static_cast<TR*>(a.dr) + at, q, t, tpr, D);
-    if (a.z) store_row<T, V, NV>(static_cast<T*>(a.dz) + at, dz, t, tpr, D);
-    if (a.w_post) {
-      row_sum<TPR, 1>(m, buf1, turn1);
-      const float k = m[0] * inv * rx;  // times x: xh mean(v w_post xh)
-#pragma unroll
-      for (int j = 0; j < NV; ++j)
-#pragma unroll
-        for (int e = 0; e < V; ++e)
-          v[j][e] = rx * fmaf(-k, to_f(x[j].v[e]), v[j][e] * wp[j][e]);
+      dsc[i] = fma(qa, u, dsc[i]);
+      r[i] = mul(qa, sc[i]);  // v
+      dwp[i] = fma(r[i], x[i], dwp[i]);
+      sm = fma(r[i], u, sm);
     }
-    store_row<T, V, NV>(static_cast<T*>(a.dx) + at, v, t, tpr, D);
+    store_row<L, TR>(static_cast<TR*>(a.dr) + o, q, at, on);
+    if (a.z) store_row<L, T>(static_cast<T*>(a.dz) + o, z, at, on);
+    if (a.w_post) {
+      float m[1] = {total(sm)};
+      row_sum<L, 1>(m, buf1, turn1);
+      const F<P> k = all<P>(-(m[0] * inv));  // -mean(v w_post xh)
+#pragma unroll
+      for (int i = 0; i < N; ++i) r[i] = mul(rp, fma(k, x[i], mul(r[i], wp[i])));
+    }
+    store_row<L, T>(static_cast<T*>(a.dx) + o, r, at, on);
   }
   // partial gradients of the weights that there are: w, then w_post, then scale
   float* part = a.part + size_t(blockIdx.x) * a.D * a.weights;
-  store_partial<TPR, V, NV>(part, dw, groups, t, tpr, a.D);
-  if (a.w_post) store_partial<TPR, V, NV>(part += a.D, dwp, groups, t, tpr, a.D);
-  if (a.scale) store_partial<TPR, V, NV>(part += a.D, dsc, groups, t, tpr, a.D);
+  store_partial<L>(part, dw, groups, at);
+  if (a.w_post) store_partial<L>(part += a.D, dwp, groups, at);
+  if (a.scale) store_partial<L>(part += a.D, dsc, groups, at);
 }
 
 // 32 columns a CTA; warp i adds the parts i, i + 8, ..., then the warps are added.
@@ -249,25 +235,23 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-constexpr long long kForwardCtas = 2;  // per SM
+constexpr long long kForwardCtas = 4;  // per SM
 
 template <typename T, typename TR>
 struct Forward {
   const ResidualNormArgs& a;
   int sms;
   cudaStream_t stream;
-  template <int TPR, int NV, int V>
+  template <typename L>
   int run() {
-    const int threads = norm_threads<TPR, NV, V>(a.D), per = TPR ? kNormThreads / TPR : 1;
-    const long long groups = (a.rows + per - 1) / per;
-    const int grid = int(groups < kForwardCtas * sms ? groups : kForwardCtas * sms);
-    constexpr size_t kBytes = 2 * sizeof(T) + sizeof(TR);  // staged of a channel
-    constexpr size_t kThread = kStaged<NV, V> ? stages(kBytes) * NV * V * kBytes : 0;
-    constexpr int kMost = TPR ? kNormThreads : kNormMaxThreads;
-    if (!raise_smem<&residual_norm_kernel<TPR, NV, V, T, TR>>(kThread * kMost)) return GDN_ERR_LAUNCH;
-    residual_norm_kernel<TPR, NV, V, T, TR><<<grid, threads, kThread * threads, stream>>>(a);
+    const long long groups = (a.rows + L::kRows - 1) / L::kRows;
+    const int grid = int(std::min(groups, kForwardCtas * sms));
+    constexpr size_t smem = ring_bytes<L>(2 * sizeof(T) + sizeof(TR));
+    if (!raise_smem<&residual_norm_kernel<L, T, TR>>(smem)) return GDN_ERR_LAUNCH;
+    residual_norm_kernel<L, T, TR><<<grid, L::TH, smem, stream>>>(a);
     return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_LAUNCH;
   }
+  int run4096() { return run<Layout<256, 256, 4, 4>>(); }
 };
 
 template <typename T, typename TR>
@@ -275,35 +259,33 @@ struct Backward {
   const ResidualNormArgs& a;
   int sms;
   cudaStream_t stream;
-  template <int TPR, int NV, int V>
+  template <typename L>
   int run() {
-    const int threads = norm_threads<TPR, NV, V>(a.D), per = TPR ? kNormThreads / TPR : 1;
-    const long long groups = (a.rows + per - 1) / per;
-    const int most = norm_max_parts(a.rows, a.D);
-    const int grid = int(groups < most ? groups : most);
-    constexpr size_t kBytes = 3 * sizeof(T) + 2 * sizeof(TR);  // staged of a channel
-    constexpr size_t kThread = kStaged<NV, V> ? stages(kBytes) * NV * V * kBytes : 0;
-    constexpr int kMost = TPR ? kNormThreads : kNormMaxThreads;
-    if (!raise_smem<&residual_norm_backward_kernel<TPR, NV, V, T, TR>>(kThread * kMost)) return GDN_ERR_LAUNCH;
-    residual_norm_backward_kernel<TPR, NV, V, T, TR><<<grid, threads, kThread * threads, stream>>>(a);
+    const long long groups = (a.rows + L::kRows - 1) / L::kRows;
+    const int grid = int(std::min<long long>(groups, norm_max_parts(a.rows, a.D)));
+    constexpr size_t smem = ring_bytes<L>(3 * sizeof(T) + 2 * sizeof(TR));
+    if (!raise_smem<&residual_norm_backward_kernel<L, T, TR>>(smem)) return GDN_ERR_LAUNCH;
+    residual_norm_backward_kernel<L, T, TR><<<grid, L::TH, smem, stream>>>(a);
     if (cudaGetLastError() != cudaSuccess) return GDN_ERR_LAUNCH;
     float* dst[3] = {a.dw, a.w_post ? a.dw_post : a.dscale, a.dscale};
     return launch_reduce_parts(a.part, grid, a.D * a.weights, dst, a.D, stream);
   }
+  int run4096() { return run<Layout<512, 512, 2, 4>>(); }
 };
 
-bool wide_ok(const ResidualNormArgs& a) {
-  const void* p[] = {a.x, a.r, a.z, a.w, a.w_post, a.scale, a.y, a.r_out, a.dy, a.dr_out,
-                     a.dx, a.dr, a.dz, a.part};
-  uintptr_t all = 0;
-  for (const void* q : p) all |= reinterpret_cast<uintptr_t>(q);
-  return (all & 15) == 0;
+// Whether every array starts on four elements.
+bool wide_ok(const ResidualNormArgs& a, int dtype, int r_dtype) {
+  const uintptr_t e = dtype == GDN_BF16 ? 8 : 16, er = r_dtype == GDN_BF16 ? 8 : 16;
+  return aligned(a.x, e) && aligned(a.z, e) && aligned(a.y, e) && aligned(a.dy, e) &&
+         aligned(a.dx, e) && aligned(a.dz, e) && aligned(a.r, er) && aligned(a.r_out, er) &&
+         aligned(a.dr_out, er) && aligned(a.dr, er) && aligned(a.w, 16) && aligned(a.w_post, 16) &&
+         aligned(a.scale, 16);
 }
 
 template <template <typename, typename> class Run>
 int dispatch(const ResidualNormArgs& a, int dtype, int r_dtype, int sms, cudaStream_t stream) {
   using B = __nv_bfloat16;
-  const bool wide = wide_ok(a);
+  const bool wide = wide_ok(a, dtype, r_dtype);
   if (dtype == GDN_F32) return with_layout(a.D, wide, Run<float, float>{a, sms, stream});
   return r_dtype == GDN_BF16 ? with_layout(a.D, wide, Run<B, B>{a, sms, stream})
                              : with_layout(a.D, wide, Run<B, float>{a, sms, stream});

@@ -46,6 +46,13 @@ __device__ __forceinline__ F<2> add(F<2> a, F<2> b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)));
   return pair(r);
 }
+template <int V>
+__device__ __forceinline__ F<V> all(float x) {
+  F<V> r;
+#pragma unroll
+  for (int e = 0; e < V; ++e) r.v[e] = x;
+  return r;
+}
 __device__ __forceinline__ F<1> fma(F<1> a, F<1> b, F<1> c) { return {{fmaf(a.v[0], b.v[0], c.v[0])}}; }
 __device__ __forceinline__ F<1> mul(F<1> a, F<1> b) { return {{a.v[0] * b.v[0]}}; }
 __device__ __forceinline__ F<1> add(F<1> a, F<1> b) { return {{a.v[0] + b.v[0]}}; }
@@ -82,8 +89,14 @@ template <typename T, int V>
 __device__ __forceinline__ Vec<T, V> load(const T* p) {
   return *reinterpret_cast<const Vec<T, V>*>(p);
 }
-// Starts an asynchronous copy of one E (4, 8 or 16 bytes) to shared memory, or
-// zeros it (bytes 0; nothing is read then).
+// Starts an asynchronous copy of one E (4, 8 or 16 bytes) to shared memory.
+template <typename E>
+__device__ __forceinline__ void copy_async(E* dst, const E* src) {
+  const unsigned d = static_cast<unsigned>(__cvta_generic_to_shared(dst));
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(d), "l"(src), "n"(sizeof(E))
+               : "memory");
+}
+// The same, or zeros (bytes 0; nothing is read then).
 template <typename E>
 __device__ __forceinline__ void copy_async(E* dst, const E* src, int bytes) {
   const unsigned d = static_cast<unsigned>(__cvta_generic_to_shared(dst));
