@@ -156,6 +156,7 @@ __global__ void __launch_bounds__(L::TH) gated_norm_backward_kernel(const GatedN
       store_row<L, T>(static_cast<T*>(a.dz) + o, z, at, on);
     }
   }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   store_partial<L>(a.part + size_t(blockIdx.x) * a.D, dw, groups, at);
 }
 

@@ -212,6 +212,7 @@ __global__ void __launch_bounds__(L::TH) residual_norm_backward_kernel(const Res
     }
     store_row<L, T>(static_cast<T*>(a.dx) + o, r, at, on);
   }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // partial gradients of the weights that there are: w, then w_post, then scale
   float* part = a.part + size_t(blockIdx.x) * a.D * a.weights;
   store_partial<L>(part, dw, groups, at);
@@ -219,20 +220,28 @@ __global__ void __launch_bounds__(L::TH) residual_norm_backward_kernel(const Res
   if (a.scale) store_partial<L>(part += a.D, dsc, groups, at);
 }
 
-// 32 columns a CTA; warp i adds the parts i, i + 8, ..., then the warps are added.
-__global__ void __launch_bounds__(256)
+// 32 columns a CTA; warp i adds the parts i, i + 32, ..., then the warps are added.
+// The launch may start before the parts are complete: it waits for the launch
+// before it first.
+constexpr int kReduceWarps = 32;
+__global__ void __launch_bounds__(32 * kReduceWarps)
     reduce_parts_kernel(const float* part, int n, int cols, float* d0, float* d1, float* d2, int D) {
-  __shared__ float sum[8][32];
+  __shared__ float sum[kReduceWarps][33];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
   float s = 0.f;
-  if (c < cols)
-    for (int p = w; p < n; p += 8) s += part[size_t(p) * cols + c];
+  if (c < cols) {
+#pragma unroll 10
+    for (int p = w; p < n; p += kReduceWarps) s += part[size_t(p) * cols + c];
+  }
   sum[w][lane] = s;
   __syncthreads();
-  if (w == 0 && c < cols) {
-    for (int i = 1; i < 8; ++i) s += sum[i][lane];
-    (c < D ? d0 : c < 2 * D ? d1 : d2)[c % D] = s;
-  }
+  // warp w adds column w: lane i has the sum of warp i
+  s = sum[lane][w];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  const int col = blockIdx.x * 32 + w;
+  if (lane == 0 && col < cols) (col < D ? d0 : col < 2 * D ? d1 : d2)[col % D] = s;
 }
 
 constexpr long long kForwardCtas = 4;  // per SM
@@ -296,9 +305,20 @@ int dispatch(const ResidualNormArgs& a, int dtype, int r_dtype, int sms, cudaStr
 int launch_reduce_parts(const float* part, int n, int cols, float* const* dst, int D,
                         cudaStream_t stream) {
   const int weights = cols / D;
-  reduce_parts_kernel<<<(cols + 31) / 32, 256, 0, stream>>>(
-      part, n, cols, dst[0], weights > 1 ? dst[1] : nullptr, weights > 2 ? dst[2] : nullptr, D);
-  return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_LAUNCH;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((cols + 31) / 32);
+  cfg.blockDim = dim3(32 * kReduceWarps);
+  cfg.stream = stream;
+  cudaLaunchAttribute at{};  // its start overlaps the end of the launch before it
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, &reduce_parts_kernel, part, n, cols, dst[0],
+                            weights > 1 ? dst[1] : static_cast<float*>(nullptr),
+                            weights > 2 ? dst[2] : static_cast<float*>(nullptr), D) == cudaSuccess
+             ? GDN_OK
+             : GDN_ERR_LAUNCH;
 }
 
 int launch_residual_norm(const ResidualNormArgs& a, int dtype, int r_dtype, int sms,
