@@ -45,7 +45,8 @@ constexpr size_t ring_bytes(size_t bytes) {
 // This thread's place: the channel of its vector j is t V + j TPR V.
 template <typename L>
 struct Place {
-  int sub, c0, D;  // its row among the CTA's, its first channel
+  int sub;          // its row among the CTA's
+  unsigned c0, D;   // its first channel, the row's channels
   __device__ __forceinline__ explicit Place(int d)
       : sub(L::kShort ? threadIdx.x / L::TPR : 0), c0((threadIdx.x % L::TPR) * L::V), D(d) {}
   __device__ __forceinline__ bool has(int j) const { return c0 + j * L::TPR * L::V < D; }
@@ -76,13 +77,13 @@ struct Ring {
       for (int j = 0; j < L::NV; ++j)
         if (!at.has(j)) *slot(smem, s, j) = E{};
   }
-  // p: this thread's first channel of the row; a row past the end is zeros
+  // p: the row's first channel; a row past the end is zeros
   __device__ __forceinline__ static void fetch(unsigned char* smem, int stage, const T* p,
                                                const Place<L>& at, bool on) {
 #pragma unroll
     for (int j = 0; j < L::NV; ++j)
       if (at.has(j)) {
-        const E* src = reinterpret_cast<const E*>(p + j * L::TPR * L::V);
+        const E* src = reinterpret_cast<const E*>(p + (at.c0 + j * L::TPR * L::V));
         if (L::kShort)
           copy_async(slot(smem, stage, j), src, on ? int(sizeof(E)) : 0);
         else
@@ -108,7 +109,7 @@ __device__ __forceinline__ void load_row(F<L::P> (&r)[L::N], const T* p, const P
 #pragma unroll
   for (int j = 0; j < L::NV; ++j) {
     Vec<T, L::V> x{};
-    if (on && at.has(j)) x = load<T, L::V>(p + j * L::TPR * L::V);
+    if (on && at.has(j)) x = load<T, L::V>(p + (at.c0 + j * L::TPR * L::V));
     spread<L, T>(r, x, j);
   }
 }
@@ -122,7 +123,7 @@ __device__ __forceinline__ void store_row(T* p, const F<L::P> (&r)[L::N], const 
       float x[L::V];
 #pragma unroll
       for (int e = 0; e < L::V; ++e) x[e] = r[(j * L::V + e) / L::P].v[e % L::P];
-      store<T, L::V>(p + j * L::TPR * L::V, x);
+      store<T, L::V>(p + (at.c0 + j * L::TPR * L::V), x);
     }
 }
 
@@ -135,7 +136,7 @@ __device__ __forceinline__ void load_weight(F<L::P> (&w)[L::N], const float* p, 
     for (int i = 0; i < L::N; ++i) w[i] = all<L::P>(1.f);
     return;
   }
-  load_row<L, float>(w, p + at.c0, at, true);
+  load_row<L, float>(w, p, at, true);
 #pragma unroll
   for (int i = 0; i < L::N; ++i) w[i] = add(w[i], all<L::P>(offset));
 }
@@ -151,34 +152,52 @@ __device__ __forceinline__ float total(F<P> a) {
 template <typename L, int K>
 struct SumBuffer {
   static constexpr int kWarps = L::TH / 32;
-  alignas(16) float part[2][K][kWarps < 4 ? 4 : kWarps];
+  float part[2][K == 1 ? 1 : 4][kWarps];
 };
 template <typename L, int K>
 __device__ __forceinline__ void row_sum(float (&v)[K], SumBuffer<L, K>& buf, int& turn) {
-  constexpr int W = L::kShort ? L::TPR : 32;
+  constexpr int n = L::TH / 32;
+  const auto halve = [](float x, int o) { return x + __shfl_xor_sync(0xffffffffu, x, o); };
+  if constexpr (L::kShort || K == 1) {
+    constexpr int W = L::kShort ? L::TPR : 32;
 #pragma unroll
-  for (int o = W / 2; o > 0; o >>= 1)
+    for (int o = W / 2; o > 0; o >>= 1)
 #pragma unroll
-    for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
-  if constexpr (!L::kShort) {
-    constexpr int n = L::TH / 32;
-    static_assert(n % 4 == 0, "partial sums are read four at a time");
-    if ((threadIdx.x & 31) == 0)
+      for (int k = 0; k < K; ++k) v[k] = halve(v[k], o);
+    if constexpr (!L::kShort) {
+      const int lane = threadIdx.x & 31;
+      if (lane == 0) buf.part[turn][0][threadIdx.x >> 5] = v[0];
+      __syncthreads();
+      v[0] = buf.part[turn][0][lane % n];
 #pragma unroll
-      for (int k = 0; k < K; ++k) buf.part[turn][k][threadIdx.x >> 5] = v[k];
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      F<2> s = all<2>(0.f);
-#pragma unroll
-      for (int i = 0; i < n; i += 4) {
-        const Vec<float, 4> x = load<float, 4>(&buf.part[turn][k][i]);
-        s = add(s, add(F<2>{{x.v[0], x.v[1]}}, F<2>{{x.v[2], x.v[3]}}));
-      }
-      v[k] = total(s);
+      for (int o = n / 2; o > 0; o >>= 1) v[0] = halve(v[0], o);
+      turn ^= 1;
     }
+  } else {
+    // up to four values at once: two exchanges leave value k with the lanes 8 k ..
+    // 8 k + 7, so that the rest is one shuffle a step instead of K
+    static_assert(K <= 4, "four groups of eight lanes");
+    const int lane = threadIdx.x & 31, mine = lane >> 3;
+    const bool hi = lane & 16, odd = lane & 8;
+    const auto merge = [](bool second, float a, float b, int o) {
+      return (second ? b : a) + __shfl_xor_sync(0xffffffffu, second ? a : b, o);
+    };
+    const float v1 = K > 1 ? v[K > 1 ? 1 : 0] : 0.f, v2 = K > 2 ? v[K > 2 ? 2 : 0] : 0.f,
+                v3 = K > 3 ? v[K > 3 ? 3 : 0] : 0.f;
+    float x = merge(odd, merge(hi, v[0], v2, 16), merge(hi, v1, v3, 16), 8);
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) x = halve(x, o);
+    if ((lane & 7) == 0) buf.part[turn][mine][threadIdx.x >> 5] = x;
+    __syncthreads();
+    x = buf.part[turn][mine][lane & (n < 8 ? n - 1 : 7)];
+    if (n > 8) x += buf.part[turn][mine][(lane & 7) + (n > 8 ? 8 : 0)];
+#pragma unroll
+    for (int o = n < 8 ? n / 2 : 4; o > 0; o >>= 1) x = halve(x, o);
+#pragma unroll
+    for (int k = 0; k < K; ++k) v[k] = __shfl_sync(0xffffffffu, x, 8 * k);
     turn ^= 1;
   }
+  static_assert(n == 4 || n == 8 || n == 16, "warps of a CTA");
 }
 
 // 1 / (1 + exp(-z)) from the approximate power and reciprocal: a few units in
@@ -189,22 +208,28 @@ __device__ __forceinline__ float sigmoid(float z) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(p) : "f"(1.f + e));
   return p;
 }
-// The gate's value and slope.
+// The gate's value and slope: p z and p (1 + z (1 - p)), or p and p (1 - p).
 template <int P>
 __device__ __forceinline__ F<P> gate(int act, F<P> z) {
   F<P> p;
 #pragma unroll
-  for (int e = 0; e < P; ++e) p.v[e] = sigmoid(z.v[e]);
-  return act == GDN_GATE_SILU ? mul(z, p) : p;
+  for (int e = 0; e < P; ++e) {
+    p.v[e] = sigmoid(z.v[e]);
+    z.v[e] = act == GDN_GATE_SILU ? z.v[e] : 1.f;
+  }
+  return mul(z, p);
 }
 template <int P>
 __device__ __forceinline__ void gate_slope(int act, F<P> z, F<P>* a, F<P>* da) {
   F<P> p;
 #pragma unroll
-  for (int e = 0; e < P; ++e) p.v[e] = sigmoid(z.v[e]);
-  const F<P> one = all<P>(1.f), q = fma(p, all<P>(-1.f), one);
-  *a = act == GDN_GATE_SILU ? mul(z, p) : p;
-  *da = mul(p, act == GDN_GATE_SILU ? fma(z, q, one) : q);
+  for (int e = 0; e < P; ++e) {
+    p.v[e] = sigmoid(z.v[e]);
+    z.v[e] = act == GDN_GATE_SILU ? z.v[e] : 1.f;
+  }
+  const F<P> q = fma(p, all<P>(-1.f), all<P>(1.f));
+  *a = mul(z, p);
+  *da = mul(p, fma(z, q, all<P>(act == GDN_GATE_SILU ? 1.f : 0.f)));
 }
 
 // A CTA's partial sums of one weight gradient, one row of D values: its rows'
@@ -213,7 +238,7 @@ template <typename L>
 __device__ __forceinline__ void store_partial(float* part, const F<L::P> (&acc)[L::N], float* smem,
                                               const Place<L>& at) {
   if constexpr (L::kRows == 1) {
-    store_row<L, float>(part + at.c0, acc, at, true);
+    store_row<L, float>(part, acc, at, true);
   } else {
     constexpr int kRow = L::TPR * L::NV * L::V;
     __syncthreads();
@@ -225,7 +250,7 @@ __device__ __forceinline__ void store_partial(float* part, const F<L::P> (&acc)[
         smem[at.sub * kRow + at.c0 + (k / L::V) * L::TPR * L::V + k % L::V] = acc[i].v[e];
       }
     __syncthreads();
-    for (int c = threadIdx.x; c < at.D; c += L::TH) {
+    for (unsigned c = threadIdx.x; c < at.D; c += L::TH) {
       float s = 0.f;
       for (int i = 0; i < L::kRows; ++i) s += smem[i * kRow + c];
       part[c] = s;

@@ -29,7 +29,7 @@ __global__ void __launch_bounds__(L::TH) gated_norm_kernel(const GatedNormArgs a
   const auto fetch = [&] {
     if (next - at.sub < a.rows) {
       const bool on = next < a.rows;
-      const size_t o = size_t(on ? next : 0) * a.D + at.c0;
+      const size_t o = size_t(on ? next : 0) * a.D;
       RX::fetch(smem, to, static_cast<const TX*>(a.x) + o, at, on);
       if (a.z) RZ::fetch(smem, to, static_cast<const T*>(a.z) + o, at, on);
     }
@@ -48,7 +48,7 @@ __global__ void __launch_bounds__(L::TH) gated_norm_kernel(const GatedNormArgs a
   const float inv = 1.f / float(a.D);
   for (; row - at.sub < a.rows; row += stride) {
     const bool on = !L::kShort || row < a.rows;
-    const size_t o = size_t(on ? row : 0) * a.D + at.c0;
+    const size_t o = size_t(on ? row : 0) * a.D;
     F<P> x[N], z[N];
     if constexpr (L::kStaged) {
       copies_wait<kStages>();
@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(L::TH) gated_norm_backward_kernel(const GatedN
   const auto fetch = [&] {
     if (next - at.sub < a.rows) {
       const bool on = next < a.rows;
-      const size_t o = size_t(on ? next : 0) * a.D + at.c0;
+      const size_t o = size_t(on ? next : 0) * a.D;
       RX::fetch(smem, to, static_cast<const TX*>(a.x) + o, at, on);
       RD::fetch(smem, to, static_cast<const T*>(a.dy) + o, at, on);
       if (a.z) RZ::fetch(smem, to, static_cast<const T*>(a.z) + o, at, on);
@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(L::TH) gated_norm_backward_kernel(const GatedN
   const float inv = 1.f / float(a.D);
   for (; row - at.sub < a.rows; row += stride) {
     const bool on = !L::kShort || row < a.rows;
-    const size_t o = size_t(on ? row : 0) * a.D + at.c0;
+    const size_t o = size_t(on ? row : 0) * a.D;
     F<P> x[N], dy[N], z[N];
     if constexpr (L::kStaged) {
       copies_wait<kStages>();

@@ -33,7 +33,7 @@ __global__ void __launch_bounds__(L::TH) residual_norm_kernel(const ResidualNorm
   const auto fetch = [&] {
     if (next - at.sub < a.rows) {
       const bool on = next < a.rows;
-      const size_t o = size_t(on ? next : 0) * a.D + at.c0;
+      const size_t o = size_t(on ? next : 0) * a.D;
       RX::fetch(smem, to, static_cast<const T*>(a.x) + o, at, on);
       RR::fetch(smem, to, static_cast<const TR*>(a.r) + o, at, on);
       if (a.z) RZ::fetch(smem, to, static_cast<const T*>(a.z) + o, at, on);
@@ -58,7 +58,7 @@ __global__ void __launch_bounds__(L::TH) residual_norm_kernel(const ResidualNorm
   const float inv = 1.f / float(a.D);
   for (; row - at.sub < a.rows; row += stride) {
     const bool on = !L::kShort || row < a.rows;
-    const size_t o = size_t(on ? row : 0) * a.D + at.c0;
+    const size_t o = size_t(on ? row : 0) * a.D;
     F<P> x[N], r[N], z[N];
     if constexpr (L::kStaged) {
       copies_wait<kStages>();
@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(L::TH) residual_norm_backward_kernel(const Res
   const auto fetch = [&] {
     if (next - at.sub < a.rows) {
       const bool on = next < a.rows;
-      const size_t o = size_t(on ? next : 0) * a.D + at.c0;
+      const size_t o = size_t(on ? next : 0) * a.D;
       RR::fetch(smem, to, static_cast<const TR*>(a.r) + o, at, on);
       RD::fetch(smem, to, static_cast<const T*>(a.dy) + o, at, on);
       RX::fetch(smem, to, static_cast<const T*>(a.x) + o, at, on);
@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(L::TH) residual_norm_backward_kernel(const Res
   const float inv = 1.f / float(a.D);
   for (; row - at.sub < a.rows; row += stride) {
     const bool on = !L::kShort || row < a.rows;
-    const size_t o = size_t(on ? row : 0) * a.D + at.c0;
+    const size_t o = size_t(on ? row : 0) * a.D;
     F<P> x[N], z[N], dy[N], r[N], q[N];
     if constexpr (L::kStaged) {
       copies_wait<kStages>();
