@@ -349,9 +349,9 @@ int static_workspace(void** out) {
 
 namespace gdn {
 bool ensure_smem_attr(const void* func, int slot, int bytes) {
-  static std::atomic<uint64_t> done[128];  // bit d: device d, per kernel slot
+  static std::atomic<uint64_t> done[96];  // bit d: device d, per kernel slot
   int dev = 0;
-  if (slot < 0 || slot >= 128 || cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64)
+  if (slot < 0 || slot >= 96 || cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64)
     return false;
   const uint64_t bit = uint64_t(1) << dev;
   if (done[slot].load(std::memory_order_acquire) & bit) return true;
@@ -361,6 +361,21 @@ bool ensure_smem_attr(const void* func, int slot, int bytes) {
   return true;
 }
 }  // namespace gdn
+
+bool gdn::encode_rows(CUtensorMap* map, const void* base, long long rows, int cols, int box_cols,
+                      int box_rows, bool bf16) {
+  auto enc = get_encode_fn();
+  if (!enc) return false;
+  const int esize = bf16 ? 2 : 4;
+  const cuuint64_t dims[2] = {cuuint64_t(cols), cuuint64_t(rows)};
+  const cuuint64_t strides[1] = {cuuint64_t(cols) * esize};
+  const cuuint32_t box[2] = {cuuint32_t(box_cols), cuuint32_t(box_rows)};
+  const cuuint32_t estr[2] = {1, 1};
+  return enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2,
+             const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 int gdn::require_device(int* sms) {
   const int rc = check_device();

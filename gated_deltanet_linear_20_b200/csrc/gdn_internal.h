@@ -190,6 +190,11 @@ int launch_rows(const RowArgs& a, int Dk, bool vector_gate, int num_sms, cudaStr
 int rows_per_cta(long long heads, int Dv, int num_sms);
 bool rows_head_dims_ok(int Dk, int Dv);
 
+// TMA view of [rows][cols] with boxes of box_rows x box_cols (unswizzled; rows and
+// columns past the end load as zeros); false if it cannot be encoded.
+bool encode_rows(CUtensorMap* map, const void* base, long long rows, int cols, int box_cols,
+                 int box_rows, bool bf16);
+
 // Channel recurrence: GDN_OK, or a negative code.  dtype is x's, beta's and h's
 // (GDN_F32 or GDN_BF16).  The step updates a.h_T in place.
 int launch_scan(const ScanArgs& a, int dtype, int sms, cudaStream_t stream);

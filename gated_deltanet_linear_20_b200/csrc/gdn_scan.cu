@@ -25,8 +25,10 @@
 // hardware barriers, and the order of every sum is fixed: results do not
 // depend on timing.
 #include <algorithm>
+#include <initializer_list>
 #include <type_traits>
 
+#include "gdn_host.h"
 #include "gdn_internal.h"
 #include "gdn_vec.cuh"
 #include "sm100.cuh"
@@ -38,7 +40,7 @@ constexpr int kCarryTokens = GDN_SCAN_CARRY_TOKENS;
 constexpr int kWarps = 4;       // of a CTA, along time
 constexpr int kMaxCluster = 8;  // CTAs along time
 constexpr uint64_t kWaitLimitNs = 2000000000;  // of a wait for the cluster's maps
-constexpr int kScanSlot = 96;   // ensure_smem_attr: 16 kernels
+constexpr long long kTmaElements = 1 << 20;  // of a call, from which TMA pays
 
 // The map of a run of tokens for V channels: c -> A c + H.  A stays finite, so
 // that a state of zero stays out of a run whose growth passes the fp32 range.
@@ -128,6 +130,20 @@ __device__ __forceinline__ bool bar_ready(uint64_t* bar, unsigned parity) {
   return ok != 0;
 }
 
+// Waits for the phase, or gives up after the limit (*late, alike in all lanes;
+// nothing is awaited then).
+__device__ __forceinline__ void bar_wait(uint64_t* bar, unsigned parity, bool* late) {
+  if (*late || __all_sync(0xffffffffu, bar_ready(bar, parity))) return;
+  const uint64_t begin = sm100::globaltimer_ns();
+  unsigned polls = 0;
+  while (!__all_sync(0xffffffffu, bar_ready(bar, parity)))
+    if ((++polls & 255u) == 0 &&
+        __any_sync(0xffffffffu, sm100::globaltimer_ns() - begin > kWaitLimitNs)) {
+      *late = true;
+      return;
+    }
+}
+
 struct Seq {
   long long start;  // first token
   int len;
@@ -155,26 +171,33 @@ __device__ __forceinline__ bool sequence(const ScanArgs& a, int n, Seq* s) {
 // passed by then (in this CTA by __syncthreads, in the cluster because a CTA
 // sends the next tile's map only after that barrier).
 template <int V>
-struct Exchange {
+struct alignas(128) Exchange {
   uint64_t bar[2];                 // the cluster's maps of a set have arrived
-  int pad[4];
+  uint64_t full[kWarps];           // a warp's slice has arrived (TMA)
   Map<V> warp[2][kWarps][32];      // this CTA's slices, in scan order
   Map<V> cta[2][kMaxCluster][32];  // the cluster's tiles, in scan order
 };
 
-// Before the first exchange.
+// Before the first exchange and the first TMA.
 template <int V>
-__device__ __forceinline__ void exchange_init(Exchange<V>& ex, unsigned n) {
-  if (n == 1) return;
+__device__ __forceinline__ void exchange_init(Exchange<V>& ex, unsigned n, bool tma) {
+  if (n == 1 && !tma) return;
   if (threadIdx.x == 0) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
+    const auto init = [](uint64_t* bar) {
       asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(
-                       static_cast<unsigned>(__cvta_generic_to_shared(&ex.bar[i])))
+                       static_cast<unsigned>(__cvta_generic_to_shared(bar)))
                    : "memory");
+    };
+    init(&ex.bar[0]);
+    init(&ex.bar[1]);
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) init(&ex.full[i]);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  cluster_barrier();  // every CTA runs, its barriers ready, before it is written to
+  if (n > 1)
+    cluster_barrier();  // every CTA runs, its barriers ready, before it is written to
+  else
+    __syncthreads();
 }
 
 // Shares the map of this thread's slice (scan order: CTA `rank`, warp `w`) and
@@ -205,16 +228,7 @@ __device__ __forceinline__ void scan_exchange(Exchange<V>& ex, int round, const 
       for (unsigned r = w; r < n; r += kWarps)
         store_remote(&ex.cta[set][rank][lane], &ex.bar[set], r, m);
     }
-    const unsigned parity = (round >> 1) & 1;
-    if (!*late && !bar_ready(&ex.bar[set], parity)) {
-      const uint64_t begin = sm100::globaltimer_ns();
-      unsigned polls = 0;
-      while (!bar_ready(&ex.bar[set], parity))
-        if ((++polls & 255u) == 0 && sm100::globaltimer_ns() - begin > kWaitLimitNs) {
-          *late = true;
-          break;
-        }
-    }
+    bar_wait(&ex.bar[set], (round >> 1) & 1, late);
     for (unsigned r = 0; r < n; ++r) {
       if (r == rank) c = carry;
       carry = apply(ex.cta[set][r][lane], carry);
@@ -232,50 +246,81 @@ __device__ __forceinline__ void scan_exchange(Exchange<V>& ex, int round, const 
 }
 
 // Behind the last exchange: no CTA ends while another may still write to it.
-__device__ __forceinline__ void exchange_end(unsigned n, bool late, int* status) {
-  if (n == 1) return;
-  if (late && status) *status = GDN_ERR_DEVICE_TIMEOUT;
-  cluster_barrier();
+// A warp whose wait ran out waits once more for the slice it has in flight.
+__device__ __forceinline__ void exchange_end(unsigned n, bool late, int* status, uint64_t* full,
+                                             unsigned issued) {
+  if (late) {
+    if (status) *status = GDN_ERR_DEVICE_TIMEOUT;
+    bool again = false;
+    if (issued > 0) bar_wait(full, (issued - 1) & 1, &again);
+  }
+  if (n > 1) cluster_barrier();
 }
 
-// A thread's slice on its way from memory: the log decays and K arrays of T, copied
-// asynchronously into a place of the thread's own while it works on the slice
-// before, so no barrier is needed and no register waits for memory.  Copies
-// move at least 4 bytes: a single bf16 (V = 1) is loaded directly instead.
+// How a slice gets from memory to registers.
+//   kDirect  loads, one after the wait for the other (single bf16 channels: the
+//            other ways move at least 4 bytes)
+//   kCopies  each thread copies its own elements to a place of its own in shared
+//            memory (cp.async), one slice ahead
+//   kTma     one lane a warp fetches the warp's slice, S tokens x 32 V channels, by
+//            TMA, one slice ahead: what the copies cost in instructions and in
+//            the load path bounds an SM otherwise
+// Either way a warp reads only what it fetched, so no barrier is needed.
+enum Loader { kDirect, kCopies, kTma };
+
+// A tile's slices: the log decays and K arrays of T.
 template <typename T, int V, int S, int K>
-struct Stage {
-  Vec<float, V> g[S][32 * kWarps];
-  Vec<T, V> t[K][S][32 * kWarps];
+struct alignas(128) Stage {
+  Vec<float, V> g[kWarps][S][32];
+  Vec<T, V> t[K][kWarps][S][32];
 };
-template <typename T, int V>
-constexpr bool kAsync = sizeof(T) * V >= 4;
+struct ScanMaps {
+  CUtensorMap g, t[3];
+};
 
 __device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // Starts the copies of tokens 0 .. cnt - 1 of a slice at p; zeros behind them.
 template <typename E, int S>
-__device__ __forceinline__ void fetch(E (&dst)[S][32 * kWarps], const void* p, size_t stride,
-                                      int cnt) {
+__device__ __forceinline__ void fetch(E (&dst)[S][32], const void* p, size_t stride, int cnt) {
   const char* q = static_cast<const char*>(p);
+  const int lane = threadIdx.x & 31;
   if (cnt == S) {
 #pragma unroll
     for (int i = 0; i < S; ++i)
-      copy_async(&dst[i][threadIdx.x], reinterpret_cast<const E*>(q + i * stride), sizeof(E));
+      copy_async(&dst[i][lane], reinterpret_cast<const E*>(q + i * stride));
   } else {
 #pragma unroll
     for (int i = 0; i < S; ++i)
-      copy_async(&dst[i][threadIdx.x], reinterpret_cast<const E*>(i < cnt ? q + i * stride : q),
-                 i < cnt ? sizeof(E) : 0);
+      copy_async(&dst[i][lane], reinterpret_cast<const E*>(i < cnt ? q + i * stride : q),
+                 i < cnt ? int(sizeof(E)) : 0);
   }
 }
 
-// The slice's elements in registers: from the stage, or (async false) from memory.
-template <bool ASYNC, typename E, int S>
-__device__ __forceinline__ void take(E (&r)[S], const E (&src)[S][32 * kWarps], const void* p,
-                                     size_t stride, int cnt) {
-  if constexpr (ASYNC) {
+// TMA box of the map at (channel c, token row), counted by bar.
+__device__ __forceinline__ void tma_rows(void* dst, const CUtensorMap* map, uint64_t* bar, int c,
+                                         int row) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(static_cast<unsigned>(__cvta_generic_to_shared(dst))),
+      "l"(reinterpret_cast<uint64_t>(map)),
+      "r"(static_cast<unsigned>(__cvta_generic_to_shared(bar))), "r"(c), "r"(row)
+      : "memory");
+}
+
+// The slice's elements in registers: from the stage (tokens >= cnt of a TMA box
+// are another sequence's: zeros instead), or directly.
+template <int LOAD, typename E, int S>
+__device__ __forceinline__ void take(E (&r)[S], const E (&src)[S][32], const void* p, size_t stride,
+                                     int cnt) {
+  if constexpr (LOAD != kDirect) {
 #pragma unroll
-    for (int i = 0; i < S; ++i) r[i] = src[i][threadIdx.x];
+    for (int i = 0; i < S; ++i) r[i] = src[i][threadIdx.x & 31];
+    if (LOAD == kTma && cnt < S) {
+#pragma unroll
+      for (int i = 0; i < S; ++i)
+        if (i >= cnt) r[i] = E{};
+    }
   } else {
     const char* q = static_cast<const char*>(p);
 #pragma unroll
@@ -286,10 +331,10 @@ __device__ __forceinline__ void take(E (&r)[S], const E (&src)[S][32 * kWarps], 
   }
 }
 
-template <typename T, int V, int S, bool BETA>
-__global__ void __launch_bounds__(32 * kWarps, 4) scan_kernel(const ScanArgs a) {
-  constexpr bool kStaged = kAsync<T, V>;
-  extern __shared__ __align__(16) unsigned char smem[];
+template <typename T, int V, int S, bool BETA, int LOAD>
+__global__ void __launch_bounds__(32 * kWarps, 4)
+    scan_kernel(const ScanArgs a, const __grid_constant__ ScanMaps maps) {
+  extern __shared__ __align__(128) unsigned char smem[];
   auto& ex = *reinterpret_cast<Exchange<V>*>(smem);
   auto& st = *reinterpret_cast<Stage<T, V, S, BETA ? 2 : 1>*>(smem + sizeof(Exchange<V>));
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
@@ -303,7 +348,7 @@ __global__ void __launch_bounds__(32 * kWarps, 4) scan_kernel(const ScanArgs a) 
     if (a.status && threadIdx.x == 0 && rank == 0) *a.status = GDN_ERR_SHAPE;
     return;
   }
-  exchange_init(ex, n);
+  exchange_init(ex, n, LOAD == kTma);
   F<V> carry{};
   if (a.h0) carry = to_f(load<float, V>(a.h0 + (size_t)seq * a.C + c0));
   constexpr int tile = kWarps * S;
@@ -311,6 +356,8 @@ __global__ void __launch_bounds__(32 * kWarps, 4) scan_kernel(const ScanArgs a) 
   const size_t gs = size_t(a.C) * 4, ts = size_t(a.C) * sizeof(T);
   int t0 = int(rank) * tile + w * S, cnt = 0;
   const char *pg = nullptr, *px = nullptr, *pb = nullptr;  // this thread's slice
+  bool late = false;    // a wait ran out: nothing more is fetched or awaited
+  unsigned issued = 0;  // slices fetched by TMA
   // the slice at token t0: tokens past the end are g = x = 0, which leaves the
   // state as it is; cnt is the same in every lane
   const auto place = [&] {
@@ -319,22 +366,31 @@ __global__ void __launch_bounds__(32 * kWarps, 4) scan_kernel(const ScanArgs a) 
     pg = reinterpret_cast<const char*>(a.g + at);
     px = reinterpret_cast<const char*>(static_cast<const T*>(a.x) + at);
     if (BETA) pb = reinterpret_cast<const char*>(static_cast<const T*>(a.beta) + at);
-    if constexpr (kStaged) {
-      fetch(st.g, pg, gs, cnt);
-      fetch(st.t[0], px, ts, cnt);
-      if constexpr (BETA) fetch(st.t[1], pb, ts, cnt);
+    if constexpr (LOAD == kCopies) {
+      fetch(st.g[w], pg, gs, cnt);
+      fetch(st.t[0][w], px, ts, cnt);
+      if constexpr (BETA) fetch(st.t[1][w], pb, ts, cnt);
+    }
+    if (LOAD == kTma && cnt > 0 && !late) ++issued;
+    if (LOAD == kTma && cnt > 0 && !late && lane == 0) {
+      const int c = (id % a.cblocks) * 32 * V, row = int(s.start) + t0;
+      bar_expect(&ex.full[w], sizeof(st.g[w]) + (BETA ? 2 : 1) * sizeof(st.t[0][w]));
+      tma_rows(&st.g[w], &maps.g, &ex.full[w], c, row);
+      tma_rows(&st.t[0][w], &maps.t[0], &ex.full[w], c, row);
+      if (BETA) tma_rows(&st.t[BETA ? 1 : 0][w], &maps.t[1], &ex.full[w], c, row);
     }
   };
   if (s.len > 0) place();
   int round = 0;
-  bool late = false;
   for (int base = 0; base < s.len; base += step, ++round) {
-    if (kStaged) copies_done();
+    if (LOAD == kCopies) copies_done();
+    if (LOAD == kTma && cnt > 0) bar_wait(&ex.full[w], (issued - 1) & 1, &late);
     Vec<float, V> g[S];
     Vec<T, V> x[S], b[S];
-    take<kStaged>(g, st.g, pg, gs, cnt);
-    take<kStaged>(x, st.t[0], px, ts, cnt);
-    if (BETA) take<kStaged>(b, st.t[BETA ? 1 : 0], pb, ts, cnt);
+    take<LOAD>(g, st.g[w], pg, gs, cnt);
+    take<LOAD>(x, st.t[0][w], px, ts, cnt);
+    if (BETA) take<LOAD>(b, st.t[BETA ? 1 : 0][w], pb, ts, cnt);
+    if (LOAD == kTma) __syncwarp();  // the next fetch overwrites what every lane has taken
     const int now = t0, have = cnt;
     t0 += step;
     if (base + step < s.len) place();  // in flight while this slice is worked on
@@ -370,19 +426,19 @@ __global__ void __launch_bounds__(32 * kWarps, 4) scan_kernel(const ScanArgs a) 
   }
   if (a.h_T && rank == 0 && w == 0 && on)
     store<float, V>(a.h_T + (size_t)seq * a.C + c0, carry.v);
-  exchange_end(n, late, a.status);
+  exchange_end(n, late, a.status, &ex.full[w], issued);
 }
 
 // Backward: the same walk from the sequence's end.  What passes a token
 // boundary is mu_t = alpha_t lam_t.  h_{t-1} is rebuilt in 32 bits from the
 // states that the forward pass kept every 16 tokens: reading them costs 4/16
 // byte an element, reading h itself 2 to 4 and, in bf16, its rounding in dg.
-template <typename T, int V, int S, bool BETA>
-__global__ void __launch_bounds__(32 * kWarps, 4) scan_backward_kernel(const ScanBackwardArgs a) {
-  constexpr bool kStaged = kAsync<T, V>;
+template <typename T, int V, int S, bool BETA, int LOAD>
+__global__ void __launch_bounds__(32 * kWarps, 4)
+    scan_backward_kernel(const ScanBackwardArgs a, const __grid_constant__ ScanMaps maps) {
   // the later slices of a kept state's 16 tokens start from the slices before
   constexpr int M = kCarryTokens / S;
-  extern __shared__ __align__(16) unsigned char smem[];
+  extern __shared__ __align__(128) unsigned char smem[];
   auto& ex = *reinterpret_cast<Exchange<V>*>(smem);
   auto& fwd = *reinterpret_cast<Map<V>(*)[2][kWarps][32]>(smem + sizeof(Exchange<V>));
   auto& st = *reinterpret_cast<Stage<T, V, S, BETA ? 3 : 2>*>(smem + sizeof(Exchange<V>) +
@@ -399,7 +455,7 @@ __global__ void __launch_bounds__(32 * kWarps, 4) scan_backward_kernel(const Sca
     if (f.status && threadIdx.x == 0 && rank == 0) *f.status = GDN_ERR_SHAPE;
     return;
   }
-  exchange_init(ex, n);
+  exchange_init(ex, n, LOAD == kTma);
   F<V> carry{};
   if (a.dh_T) carry = to_f(load<float, V>(a.dh_T + (size_t)seq * f.C + c0));
   constexpr int tile = kWarps * S;
@@ -410,6 +466,8 @@ __global__ void __launch_bounds__(32 * kWarps, 4) scan_backward_kernel(const Sca
   const char *pg = nullptr, *pd = nullptr, *px = nullptr, *pb = nullptr;
   size_t at = 0;
   Vec<float, V> kept{};
+  bool late = false;
+  unsigned issued = 0;
   const auto place = [&] {
     const int t0 = ti * tile + sw * S;
     cnt = ti >= 0 ? min(max(s.len - t0, 0), S) : 0;
@@ -418,27 +476,37 @@ __global__ void __launch_bounds__(32 * kWarps, 4) scan_backward_kernel(const Sca
     pd = reinterpret_cast<const char*>(static_cast<const T*>(a.dh) + at);
     px = reinterpret_cast<const char*>(static_cast<const T*>(f.x) + at);
     if (BETA) pb = reinterpret_cast<const char*>(static_cast<const T*>(f.beta) + at);
-    if constexpr (kStaged) {
-      fetch(st.g, pg, gs, cnt);
-      fetch(st.t[0], pd, ts, cnt);
-      fetch(st.t[1], px, ts, cnt);
-      if constexpr (BETA) fetch(st.t[2], pb, ts, cnt);
+    if constexpr (LOAD == kCopies) {
+      fetch(st.g[w], pg, gs, cnt);
+      fetch(st.t[0][w], pd, ts, cnt);
+      fetch(st.t[1][w], px, ts, cnt);
+      if constexpr (BETA) fetch(st.t[2][w], pb, ts, cnt);
+    }
+    if (LOAD == kTma && cnt > 0 && !late) ++issued;
+    if (LOAD == kTma && cnt > 0 && !late && lane == 0) {
+      const int c = (id % f.cblocks) * 32 * V, row = int(s.start) + t0;
+      bar_expect(&ex.full[w], sizeof(st.g[w]) + (BETA ? 3 : 2) * sizeof(st.t[0][w]));
+      tma_rows(&st.g[w], &maps.g, &ex.full[w], c, row);
+      tma_rows(&st.t[0][w], &maps.t[0], &ex.full[w], c, row);
+      tma_rows(&st.t[1][w], &maps.t[1], &ex.full[w], c, row);
+      if (BETA) tma_rows(&st.t[BETA ? 2 : 0][w], &maps.t[2], &ex.full[w], c, row);
     }
     if (cnt > 0)
       kept = load<float, V>(f.carries + size_t(s.carry_row + t0 / kCarryTokens) * f.C + c0);
   };
   if (tiles > 0) place();
   int round = 0;
-  bool late = false;
   for (int first = 0; first < tiles; first += int(n), ++round) {
     const int set = round & 1;
-    if (kStaged) copies_done();
+    if (LOAD == kCopies) copies_done();
+    if (LOAD == kTma && cnt > 0) bar_wait(&ex.full[w], (issued - 1) & 1, &late);
     Vec<float, V> g[S];
     Vec<T, V> x[S], b[S], d[S];
-    take<kStaged>(g, st.g, pg, gs, cnt);
-    take<kStaged>(d, st.t[0], pd, ts, cnt);
-    take<kStaged>(x, st.t[1], px, ts, cnt);
-    if (BETA) take<kStaged>(b, st.t[BETA ? 2 : 0], pb, ts, cnt);
+    take<LOAD>(g, st.g[w], pg, gs, cnt);
+    take<LOAD>(d, st.t[0][w], pd, ts, cnt);
+    take<LOAD>(x, st.t[1][w], px, ts, cnt);
+    if (BETA) take<LOAD>(b, st.t[BETA ? 2 : 0][w], pb, ts, cnt);
+    if (LOAD == kTma) __syncwarp();
     F<V> h = to_f(kept), mu;
     const size_t out = at;
     const int have = cnt;
@@ -483,7 +551,7 @@ __global__ void __launch_bounds__(32 * kWarps, 4) scan_backward_kernel(const Sca
   }
   if (a.dh0 && rank == 0 && w == 0 && on)
     store<float, V>(a.dh0 + (size_t)seq * f.C + c0, carry.v);
-  exchange_end(n, late, f.status);
+  exchange_end(n, late, f.status, &ex.full[w], issued);
 }
 
 // One token: elementwise, V channels a thread.
@@ -515,12 +583,26 @@ int pick_cluster(const ScanArgs& a, int S, long long chains, int sms) {
   return n;
 }
 
-template <typename Args>
-bool launch_cluster(void (*kernel)(const Args), const Args& args, size_t smem, int slot,
-                    long long ctas, int n, cudaStream_t stream) {
-  if (smem > 48 * 1024 &&
-      !ensure_smem_attr(reinterpret_cast<const void*>(kernel), slot, int(smem)))
-    return false;
+// go(has beta, loader), both as types.
+template <typename T, int V, typename Go>
+bool dispatch_load(bool beta, bool tma, Go&& go) {
+  const auto with = [&](auto b) {
+    if constexpr (V == 1 && sizeof(T) == 2) {
+      return go(b, std::integral_constant<int, kDirect>{});
+    } else if constexpr (V == 2) {
+      return tma ? go(b, std::integral_constant<int, kTma>{})
+                 : go(b, std::integral_constant<int, kCopies>{});
+    } else {
+      return go(b, std::integral_constant<int, kCopies>{});
+    }
+  };
+  return beta ? with(std::true_type{}) : with(std::false_type{});
+}
+
+template <auto Kernel, typename Args>
+bool launch_cluster(const Args& args, const ScanMaps& maps, size_t smem, long long ctas, int n,
+                    cudaStream_t stream) {
+  if (!raise_smem<Kernel>(smem)) return false;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(unsigned(ctas * n));
   cfg.blockDim = dim3(32 * kWarps);
@@ -532,7 +614,16 @@ bool launch_cluster(void (*kernel)(const Args), const Args& args, size_t smem, i
   at.val.clusterDim.y = at.val.clusterDim.z = 1;
   cfg.attrs = &at;
   cfg.numAttrs = n > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kernel, args) == cudaSuccess;
+  return cudaLaunchKernelEx(&cfg, Kernel, args, maps) == cudaSuccess;
+}
+
+// TMA wants 16-byte rows and bases; encoding its maps costs the host a few
+// microseconds, which only calls of some size hide.
+bool tma_ok(const ScanArgs& a, long long rows, int esize, std::initializer_list<const void*> ins) {
+  if (a.C < 64 || a.C * esize % 16 != 0 || rows * a.C < kTmaElements) return false;
+  for (const void* p : ins)
+    if (!aligned(p, 16)) return false;
+  return aligned(a.g, 16);
 }
 
 template <typename T, int V, int S>
@@ -541,31 +632,50 @@ int run_scan(ScanArgs a, int sms, cudaStream_t stream) {
   const long long chains = (long long)a.cblocks * a.N;
   if (chains * kMaxCluster > 0x7fffffffLL) return GDN_ERR_SHAPE;
   const int n = pick_cluster(a, S, chains, sms);
-  const auto go = [&](auto beta) {
+  const long long rows = a.cu_seqlens ? a.T : (long long)a.N * a.T;
+  constexpr bool bf16 = sizeof(T) == 2;
+  ScanMaps maps{};
+  bool tma = V == 2 && tma_ok(a, rows, sizeof(T), {a.x, a.beta});
+  if (tma)
+    tma = encode_rows(&maps.g, a.g, rows, a.C, 64, S, false) &&
+          encode_rows(&maps.t[0], a.x, rows, a.C, 64, S, bf16) &&
+          (!a.beta || encode_rows(&maps.t[1], a.beta, rows, a.C, 64, S, bf16));
+  const auto go = [&](auto beta, auto load) {
     constexpr bool kBeta = decltype(beta)::value;
+    constexpr int kLoad = decltype(load)::value;
     constexpr size_t smem =
-        sizeof(Exchange<V>) + (kAsync<T, V> ? sizeof(Stage<T, V, S, kBeta ? 2 : 1>) : 0);
-    constexpr int slot = kScanSlot + (sizeof(T) == 4) * 4 + (V == 2) * 2 + kBeta;
-    return launch_cluster(&scan_kernel<T, V, S, kBeta>, a, smem, slot, chains, n, stream);
+        sizeof(Exchange<V>) + (kLoad != kDirect ? sizeof(Stage<T, V, S, kBeta ? 2 : 1>) : 0);
+    return launch_cluster<&scan_kernel<T, V, S, kBeta, kLoad>>(a, maps, smem, chains, n, stream);
   };
-  return (a.beta ? go(std::true_type{}) : go(std::false_type{})) ? GDN_OK : GDN_ERR_LAUNCH;
+  return dispatch_load<T, V>(a.beta != nullptr, tma, go) ? GDN_OK : GDN_ERR_LAUNCH;
 }
 
 template <typename T, int V, int S>
 int run_backward(ScanBackwardArgs a, int sms, cudaStream_t stream) {
   static_assert(kWarps * S % kCarryTokens == 0, "a tile starts at a kept state");
-  a.f.cblocks = (a.f.C + 32 * V - 1) / (32 * V);
-  const long long chains = (long long)a.f.cblocks * a.f.N;
+  ScanArgs& f = a.f;
+  f.cblocks = (f.C + 32 * V - 1) / (32 * V);
+  const long long chains = (long long)f.cblocks * f.N;
   if (chains * kMaxCluster > 0x7fffffffLL) return GDN_ERR_SHAPE;
-  const int n = pick_cluster(a.f, S, chains, sms);
-  const auto go = [&](auto beta) {
+  const int n = pick_cluster(f, S, chains, sms);
+  const long long rows = f.cu_seqlens ? f.T : (long long)f.N * f.T;
+  constexpr bool bf16 = sizeof(T) == 2;
+  ScanMaps maps{};
+  bool tma = V == 2 && tma_ok(f, rows, sizeof(T), {f.x, f.beta, a.dh});
+  if (tma)
+    tma = encode_rows(&maps.g, f.g, rows, f.C, 64, S, false) &&
+          encode_rows(&maps.t[0], a.dh, rows, f.C, 64, S, bf16) &&
+          encode_rows(&maps.t[1], f.x, rows, f.C, 64, S, bf16) &&
+          (!f.beta || encode_rows(&maps.t[2], f.beta, rows, f.C, 64, S, bf16));
+  const auto go = [&](auto beta, auto load) {
     constexpr bool kBeta = decltype(beta)::value;
+    constexpr int kLoad = decltype(load)::value;
     constexpr size_t smem = sizeof(Exchange<V>) + sizeof(Map<V>[2][kWarps][32]) +
-                            (kAsync<T, V> ? sizeof(Stage<T, V, S, kBeta ? 3 : 2>) : 0);
-    constexpr int slot = kScanSlot + 8 + (sizeof(T) == 4) * 4 + (V == 2) * 2 + kBeta;
-    return launch_cluster(&scan_backward_kernel<T, V, S, kBeta>, a, smem, slot, chains, n, stream);
+                            (kLoad != kDirect ? sizeof(Stage<T, V, S, kBeta ? 3 : 2>) : 0);
+    return launch_cluster<&scan_backward_kernel<T, V, S, kBeta, kLoad>>(a, maps, smem, chains, n,
+                                                                        stream);
   };
-  return (a.f.beta ? go(std::true_type{}) : go(std::false_type{})) ? GDN_OK : GDN_ERR_LAUNCH;
+  return dispatch_load<T, V>(f.beta != nullptr, tma, go) ? GDN_OK : GDN_ERR_LAUNCH;
 }
 
 // Two channels a thread where the channel count is even and every array starts
