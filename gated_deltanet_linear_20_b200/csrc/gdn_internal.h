@@ -114,6 +114,7 @@ struct ScanArgs {
   int N, T, C;
   int cblocks;           // channel blocks per sequence (set by the launch)
   int* status;           // may be null
+  bool sorted = false;   // packed sequences longest first (set by the launch)
 };
 struct ScanBackwardArgs {
   ScanArgs f;            // inputs of the forward call and its carries

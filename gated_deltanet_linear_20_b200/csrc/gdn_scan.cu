@@ -40,7 +40,8 @@ constexpr int kCarryTokens = GDN_SCAN_CARRY_TOKENS;
 constexpr int kWarps = 4;       // of a CTA, along time
 constexpr int kMaxCluster = 8;  // CTAs along time
 constexpr uint64_t kWaitLimitNs = 2000000000;  // of a wait for the cluster's maps
-constexpr long long kTmaElements = 1 << 20;  // of a call, from which TMA pays
+constexpr long long kTmaElements = 1 << 17;  // of a call, from which TMA is used
+constexpr int kMaxSorted = 128;  // packed sequences that are started longest first
 
 // The map of a run of tokens for V channels: c -> A c + H.  A stays finite, so
 // that a state of zero stays out of a run whose growth passes the fp32 range.
@@ -164,6 +165,23 @@ __device__ __forceinline__ bool sequence(const ScanArgs& a, int n, Seq* s) {
   s->len = e - b;
   s->carry_row = b / kCarryTokens + n;
   return true;
+}
+
+// The sequence that CTA group r works on: with more CTAs than are resident, packed
+// sequences start longest first (ties in order), so that a long one does not run
+// alone at the end.  The same answer in every thread of every CTA of r.
+__device__ __forceinline__ int pick_sequence(const ScanArgs& a, int r) {
+  if (!a.sorted) return r;
+  __shared__ int len[kMaxSorted], found;
+  const int t = threadIdx.x;  // kMaxSorted threads
+  const int mine = t < a.N ? a.cu_seqlens[t + 1] - a.cu_seqlens[t] : 0;
+  len[t] = mine;
+  __syncthreads();
+  int rank = 0;
+  for (int j = 0; j < a.N; ++j) rank += len[j] > mine || (len[j] == mine && j < t);
+  if (t < a.N && rank == r) found = t;
+  __syncthreads();
+  return found;
 }
 
 // Shared memory of the exchange: two sets, used in turn.  A set is written again
@@ -339,7 +357,7 @@ __global__ void __launch_bounds__(32 * kWarps, 4)
   auto& st = *reinterpret_cast<Stage<T, V, S, BETA ? 2 : 1>*>(smem + sizeof(Exchange<V>));
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const unsigned n = cluster_size(), rank = cluster_rank();
-  const int id = blockIdx.x / n, seq = id / a.cblocks;
+  const int id = blockIdx.x / n, seq = pick_sequence(a, id / a.cblocks);
   int c0 = (id % a.cblocks) * 32 * V + lane * V;
   const bool on = c0 < a.C;
   if (!on) c0 = a.C - V;  // lanes past the last channel repeat it and store nothing
@@ -446,7 +464,7 @@ __global__ void __launch_bounds__(32 * kWarps, 4)
   const ScanArgs& f = a.f;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const unsigned n = cluster_size(), rank = cluster_rank();
-  const int id = blockIdx.x / n, seq = id / f.cblocks;
+  const int id = blockIdx.x / n, seq = pick_sequence(f, id / f.cblocks);
   int c0 = (id % f.cblocks) * 32 * V + lane * V;
   const bool on = c0 < f.C;
   if (!on) c0 = f.C - V;
@@ -574,12 +592,13 @@ __global__ void __launch_bounds__(256) scan_step_kernel(const T* x, const float*
   store<T, V>(h + i, r);
 }
 
-// CTAs along time: the fewest that give every SM four, as long as each has
-// tokens of a sequence of average length.
+// CTAs along time: as many, up to 8, as are all resident at once (four per SM),
+// as long as each has tokens of a sequence of average length.  4 x 4096 x 2048
+// (128 chains) forward: 88 us on 1 CTA, 62 on 2, 57 on 4, 61 on 8 (two waves).
 int pick_cluster(const ScanArgs& a, int S, long long chains, int sms) {
   const long long len = a.cu_seqlens ? std::max<long long>(1, a.T / std::max(1, a.N)) : a.T;
   int n = 1;
-  while (n < kMaxCluster && chains * n < 4LL * sms && (long long)n * kWarps * S < len) n *= 2;
+  while (n < kMaxCluster && chains * n * 2 <= 4LL * sms && (long long)n * kWarps * S < len) n *= 2;
   return n;
 }
 
@@ -617,8 +636,10 @@ bool launch_cluster(const Args& args, const ScanMaps& maps, size_t smem, long lo
   return cudaLaunchKernelEx(&cfg, Kernel, args, maps) == cudaSuccess;
 }
 
-// TMA wants 16-byte rows and bases; encoding its maps costs the host a few
-// microseconds, which only calls of some size hide.
+// TMA wants 16-byte rows and bases.  Encoding its maps takes the host some tenths
+// of a microsecond, which calls of 64 x 2048 elements and more win back (16 x 2048:
+// 5.4 us a call against 5.2, 128 x 2048: 6.4 against 6.5; backward 6.2 against 6.1
+// and 6.5 against 7.0).
 bool tma_ok(const ScanArgs& a, long long rows, int esize, std::initializer_list<const void*> ins) {
   if (a.C < 64 || a.C * esize % 16 != 0 || rows * a.C < kTmaElements) return false;
   for (const void* p : ins)
@@ -632,6 +653,7 @@ int run_scan(ScanArgs a, int sms, cudaStream_t stream) {
   const long long chains = (long long)a.cblocks * a.N;
   if (chains * kMaxCluster > 0x7fffffffLL) return GDN_ERR_SHAPE;
   const int n = pick_cluster(a, S, chains, sms);
+  a.sorted = a.cu_seqlens && a.N <= kMaxSorted && chains * n > 4LL * sms;
   const long long rows = a.cu_seqlens ? a.T : (long long)a.N * a.T;
   constexpr bool bf16 = sizeof(T) == 2;
   ScanMaps maps{};
@@ -658,6 +680,7 @@ int run_backward(ScanBackwardArgs a, int sms, cudaStream_t stream) {
   const long long chains = (long long)f.cblocks * f.N;
   if (chains * kMaxCluster > 0x7fffffffLL) return GDN_ERR_SHAPE;
   const int n = pick_cluster(f, S, chains, sms);
+  f.sorted = f.cu_seqlens && f.N <= kMaxSorted && chains * n > 4LL * sms;
   const long long rows = f.cu_seqlens ? f.T : (long long)f.N * f.T;
   constexpr bool bf16 = sizeof(T) == 2;
   ScanMaps maps{};

@@ -52,6 +52,8 @@ SIZES = [  # B, T, C: one token, ends inside a slice, a tile, a cluster's tile; 
     (1, 1, 1), (3, 1, 64), (2, 2, 65), (1, 15, 32), (1, 16, 2), (2, 17, 64), (1, 127, 63),
     (1, 128, 130), (2, 129, 34), (1, 257, 100), (1, 1000, 7), (1, 1025, 66), (2, 2500, 64),
     (5, 40, 1000), (300, 3, 65), (2, 64, 5000),
+    # large enough for TMA, whose boxes reach past channels, sequences and the end
+    (3, 100, 1000), (1, 777, 184), (9, 33, 520), (2, 1100, 72), (70, 5, 400),
 ]
 
 
@@ -75,10 +77,10 @@ def test_scan_and_gradients(B, T, C, beta, h0, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
-@pytest.mark.parametrize("C", [1, 64, 131])
+@pytest.mark.parametrize("C", [1, 64, 131, 520])
 @pytest.mark.parametrize("lens", [
     [0], [1], [0, 0, 5, 0], [16, 1, 15, 17, 33], [1] * 40, [700, 3, 0, 129, 16, 2000],
-    [31, 32, 0, 33, 64, 500, 1],
+    [31, 32, 0, 33, 64, 500, 1], [5, 90, 0, 1, 33, 16, 60, 2] * 15, [9, 1, 17] * 60,
 ], ids=lambda x: f"{len(x)}seqs{sum(x)}")
 def test_scan_varlen_and_gradients(lens, C, dtype):
     d = ref.scan_inputs(lens, C, dtype, seed=sum(lens) + C)
