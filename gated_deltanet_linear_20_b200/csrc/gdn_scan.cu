@@ -37,7 +37,6 @@ namespace gdn {
 namespace {
 
 constexpr int kCarryTokens = GDN_SCAN_CARRY_TOKENS;
-constexpr int kWarps = 4;       // of a CTA, along time
 constexpr int kMaxCluster = 8;  // CTAs along time
 constexpr uint64_t kWaitLimitNs = 2000000000;  // of a wait for the cluster's maps
 constexpr long long kTmaElements = 1 << 17;  // of a call, from which TMA is used
@@ -173,9 +172,9 @@ __device__ __forceinline__ bool sequence(const ScanArgs& a, int n, Seq* s) {
 __device__ __forceinline__ int pick_sequence(const ScanArgs& a, int r) {
   if (!a.sorted) return r;
   __shared__ int len[kMaxSorted], found;
-  const int t = threadIdx.x;  // kMaxSorted threads
+  const int t = threadIdx.x;  // of kMaxSorted or more
   const int mine = t < a.N ? a.cu_seqlens[t + 1] - a.cu_seqlens[t] : 0;
-  len[t] = mine;
+  if (t < a.N) len[t] = mine;
   __syncthreads();
   int rank = 0;
   for (int j = 0; j < a.N; ++j) rank += len[j] > mine || (len[j] == mine && j < t);
@@ -188,17 +187,17 @@ __device__ __forceinline__ int pick_sequence(const ScanArgs& a, int r) {
 // only behind the wait for the other one, which every thread that reads it has
 // passed by then (in this CTA by __syncthreads, in the cluster because a CTA
 // sends the next tile's map only after that barrier).
-template <int V>
+template <int V, int W>
 struct alignas(128) Exchange {
   uint64_t bar[2];                 // the cluster's maps of a set have arrived
-  uint64_t full[kWarps];           // a warp's slice has arrived (TMA)
-  Map<V> warp[2][kWarps][32];      // this CTA's slices, in scan order
-  Map<V> cta[2][kMaxCluster][32];  // the cluster's tiles, in scan order
+  uint64_t full[W];                // a warp's slice has arrived (TMA)
+  Map<V> warp[2][W][32];           // this CTA's slices, in scan order
+  Map<V> cta[2][W >= 4 ? kMaxCluster : 1][32];  // the cluster's tiles, in scan order
 };
 
 // Before the first exchange and the first TMA.
-template <int V>
-__device__ __forceinline__ void exchange_init(Exchange<V>& ex, unsigned n, bool tma) {
+template <int V, int W>
+__device__ __forceinline__ void exchange_init(Exchange<V, W>& ex, unsigned n, bool tma) {
   if (n == 1 && !tma) return;
   if (threadIdx.x == 0) {
     const auto init = [](uint64_t* bar) {
@@ -209,7 +208,7 @@ __device__ __forceinline__ void exchange_init(Exchange<V>& ex, unsigned n, bool 
     init(&ex.bar[0]);
     init(&ex.bar[1]);
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) init(&ex.full[i]);
+    for (int i = 0; i < W; ++i) init(&ex.full[i]);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (n > 1)
@@ -225,8 +224,8 @@ __device__ __forceinline__ void exchange_init(Exchange<V>& ex, unsigned n, bool 
 // mbarrier: a cluster barrier's release would wait for all of the CTA's stores
 // to global memory as well.  The wait is bounded; a CTA that gave up once
 // (*late) waits no more, goes on with what it has and reports it at the end.
-template <int V>
-__device__ __forceinline__ void scan_exchange(Exchange<V>& ex, int round, const Map<V>& mine,
+template <int V, int W>
+__device__ __forceinline__ void scan_exchange(Exchange<V, W>& ex, int round, const Map<V>& mine,
                                               F<V>& carry, F<V>& c, int w, int lane,
                                               unsigned rank, unsigned n, bool* late) {
   const int set = round & 1;
@@ -235,15 +234,15 @@ __device__ __forceinline__ void scan_exchange(Exchange<V>& ex, int round, const 
   __syncthreads();
   c = carry;
   if (n > 1) {
-    if (w < n) {  // warp w composes the CTA's map for the CTAs w, w + kWarps, ...
+    if (w < n) {  // warp w composes the CTA's map for the CTAs w, w + W, ...
       Map<V> m = ex.warp[set][0][lane];
 #pragma unroll
-      for (int i = 1; i < kWarps; ++i) {
+      for (int i = 1; i < W; ++i) {
         const Map<V> y = ex.warp[set][i][lane];
         m.H = apply(y, m.H);
         m.A = finite(mul(m.A, y.A));
       }
-      for (unsigned r = w; r < n; r += kWarps)
+      for (unsigned r = w; r < n; r += W)
         store_remote(&ex.cta[set][rank][lane], &ex.bar[set], r, m);
     }
     bar_wait(&ex.bar[set], (round >> 1) & 1, late);
@@ -252,11 +251,11 @@ __device__ __forceinline__ void scan_exchange(Exchange<V>& ex, int round, const 
       carry = apply(ex.cta[set][r][lane], carry);
     }
 #pragma unroll
-    for (int i = 0; i < kWarps - 1; ++i)
+    for (int i = 0; i < W - 1; ++i)
       if (i < w) c = apply(ex.warp[set][i][lane], c);
   } else {
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) {
+    for (int i = 0; i < W; ++i) {
       if (i == w) c = carry;
       carry = apply(ex.warp[set][i][lane], carry);
     }
@@ -275,45 +274,21 @@ __device__ __forceinline__ void exchange_end(unsigned n, bool late, int* status,
   if (n > 1) cluster_barrier();
 }
 
-// How a slice gets from memory to registers.
-//   kDirect  loads, one after the wait for the other (single bf16 channels: the
-//            other ways move at least 4 bytes)
-//   kCopies  each thread copies its own elements to a place of its own in shared
-//            memory (cp.async), one slice ahead
-//   kTma     one lane a warp fetches the warp's slice, S tokens x 32 V channels, by
-//            TMA, one slice ahead: what the copies cost in instructions and in
-//            the load path bounds an SM otherwise
-// Either way a warp reads only what it fetched, so no barrier is needed.
-enum Loader { kDirect, kCopies, kTma };
+// How a slice gets from memory to registers.  By TMA: one lane a warp fetches the
+// warp's slice, S tokens x 32 V channels, one slice ahead; a warp reads only what
+// it fetched, so no barrier is needed.  Else by plain loads.  (Copies by cp.async,
+// each thread its own elements, were slower than either: 32768 x 4096 forward 283
+// us against 207 by TMA; 5 x 577 x 577 in fp32 28 us against 10 by loads.)
 
 // A tile's slices: the log decays and K arrays of T.
-template <typename T, int V, int S, int K>
+template <typename T, int V, int S, int W, int K>
 struct alignas(128) Stage {
-  Vec<float, V> g[kWarps][S][32];
-  Vec<T, V> t[K][kWarps][S][32];
+  Vec<float, V> g[W][S][32];
+  Vec<T, V> t[K][W][S][32];
 };
 struct ScanMaps {
   CUtensorMap g, t[3];
 };
-
-__device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-
-// Starts the copies of tokens 0 .. cnt - 1 of a slice at p; zeros behind them.
-template <typename E, int S>
-__device__ __forceinline__ void fetch(E (&dst)[S][32], const void* p, size_t stride, int cnt) {
-  const char* q = static_cast<const char*>(p);
-  const int lane = threadIdx.x & 31;
-  if (cnt == S) {
-#pragma unroll
-    for (int i = 0; i < S; ++i)
-      copy_async(&dst[i][lane], reinterpret_cast<const E*>(q + i * stride));
-  } else {
-#pragma unroll
-    for (int i = 0; i < S; ++i)
-      copy_async(&dst[i][lane], reinterpret_cast<const E*>(i < cnt ? q + i * stride : q),
-                 i < cnt ? int(sizeof(E)) : 0);
-  }
-}
 
 // TMA box of the map at (channel c, token row), counted by bar.
 __device__ __forceinline__ void tma_rows(void* dst, const CUtensorMap* map, uint64_t* bar, int c,
@@ -328,13 +303,13 @@ __device__ __forceinline__ void tma_rows(void* dst, const CUtensorMap* map, uint
 
 // The slice's elements in registers: from the stage (tokens >= cnt of a TMA box
 // are another sequence's: zeros instead), or directly.
-template <int LOAD, typename E, int S>
+template <bool TMA, typename E, int S>
 __device__ __forceinline__ void take(E (&r)[S], const E (&src)[S][32], const void* p, size_t stride,
                                      int cnt) {
-  if constexpr (LOAD != kDirect) {
+  if constexpr (TMA) {
 #pragma unroll
     for (int i = 0; i < S; ++i) r[i] = src[i][threadIdx.x & 31];
-    if (LOAD == kTma && cnt < S) {
+    if (cnt < S) {
 #pragma unroll
       for (int i = 0; i < S; ++i)
         if (i >= cnt) r[i] = E{};
@@ -349,12 +324,12 @@ __device__ __forceinline__ void take(E (&r)[S], const E (&src)[S][32], const voi
   }
 }
 
-template <typename T, int V, int S, bool BETA, int LOAD>
-__global__ void __launch_bounds__(32 * kWarps, 4)
+template <typename T, int V, int S, int W, bool BETA, bool TMA>
+__global__ void __launch_bounds__(32 * W, 16 / W)
     scan_kernel(const ScanArgs a, const __grid_constant__ ScanMaps maps) {
   extern __shared__ __align__(128) unsigned char smem[];
-  auto& ex = *reinterpret_cast<Exchange<V>*>(smem);
-  auto& st = *reinterpret_cast<Stage<T, V, S, BETA ? 2 : 1>*>(smem + sizeof(Exchange<V>));
+  auto& ex = *reinterpret_cast<Exchange<V, W>*>(smem);
+  auto& st = *reinterpret_cast<Stage<T, V, S, W, BETA ? 2 : 1>*>(smem + sizeof(Exchange<V, W>));
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const unsigned n = cluster_size(), rank = cluster_rank();
   const int id = blockIdx.x / n, seq = pick_sequence(a, id / a.cblocks);
@@ -366,10 +341,10 @@ __global__ void __launch_bounds__(32 * kWarps, 4)
     if (a.status && threadIdx.x == 0 && rank == 0) *a.status = GDN_ERR_SHAPE;
     return;
   }
-  exchange_init(ex, n, LOAD == kTma);
+  exchange_init(ex, n, TMA);
   F<V> carry{};
   if (a.h0) carry = to_f(load<float, V>(a.h0 + (size_t)seq * a.C + c0));
-  constexpr int tile = kWarps * S;
+  constexpr int tile = W * S;
   const int step = tile * int(n);
   const size_t gs = size_t(a.C) * 4, ts = size_t(a.C) * sizeof(T);
   int t0 = int(rank) * tile + w * S, cnt = 0;
@@ -384,13 +359,8 @@ __global__ void __launch_bounds__(32 * kWarps, 4)
     pg = reinterpret_cast<const char*>(a.g + at);
     px = reinterpret_cast<const char*>(static_cast<const T*>(a.x) + at);
     if (BETA) pb = reinterpret_cast<const char*>(static_cast<const T*>(a.beta) + at);
-    if constexpr (LOAD == kCopies) {
-      fetch(st.g[w], pg, gs, cnt);
-      fetch(st.t[0][w], px, ts, cnt);
-      if constexpr (BETA) fetch(st.t[1][w], pb, ts, cnt);
-    }
-    if (LOAD == kTma && cnt > 0 && !late) ++issued;
-    if (LOAD == kTma && cnt > 0 && !late && lane == 0) {
+    if (TMA && cnt > 0 && !late) ++issued;
+    if (TMA && cnt > 0 && !late && lane == 0) {
       const int c = (id % a.cblocks) * 32 * V, row = int(s.start) + t0;
       bar_expect(&ex.full[w], sizeof(st.g[w]) + (BETA ? 2 : 1) * sizeof(st.t[0][w]));
       tma_rows(&st.g[w], &maps.g, &ex.full[w], c, row);
@@ -401,14 +371,13 @@ __global__ void __launch_bounds__(32 * kWarps, 4)
   if (s.len > 0) place();
   int round = 0;
   for (int base = 0; base < s.len; base += step, ++round) {
-    if (LOAD == kCopies) copies_done();
-    if (LOAD == kTma && cnt > 0) bar_wait(&ex.full[w], (issued - 1) & 1, &late);
+    if (TMA && cnt > 0) bar_wait(&ex.full[w], (issued - 1) & 1, &late);
     Vec<float, V> g[S];
     Vec<T, V> x[S], b[S];
-    take<LOAD>(g, st.g[w], pg, gs, cnt);
-    take<LOAD>(x, st.t[0][w], px, ts, cnt);
-    if (BETA) take<LOAD>(b, st.t[BETA ? 1 : 0][w], pb, ts, cnt);
-    if (LOAD == kTma) __syncwarp();  // the next fetch overwrites what every lane has taken
+    take<TMA>(g, st.g[w], pg, gs, cnt);
+    take<TMA>(x, st.t[0][w], px, ts, cnt);
+    if (BETA) take<TMA>(b, st.t[BETA ? 1 : 0][w], pb, ts, cnt);
+    if (TMA) __syncwarp();  // the next fetch overwrites what every lane has taken
     const int now = t0, have = cnt;
     t0 += step;
     if (base + step < s.len) place();  // in flight while this slice is worked on
@@ -422,7 +391,7 @@ __global__ void __launch_bounds__(32 * kWarps, 4)
       m.H = fma(al[i], m.H, u[i]);
     }
     m.A = finite(decay(m.A));
-    scan_exchange<V>(ex, round, m, carry, h, w, lane, rank, n, &late);
+    scan_exchange(ex, round, m, carry, h, w, lane, rank, n, &late);
     if (have > 0 && on && a.carries && now % kCarryTokens == 0)
       store<float, V>(a.carries + size_t(s.carry_row + now / kCarryTokens) * a.C + c0, h.v);
     if (a.h && on) {
@@ -451,15 +420,15 @@ __global__ void __launch_bounds__(32 * kWarps, 4)
 // boundary is mu_t = alpha_t lam_t.  h_{t-1} is rebuilt in 32 bits from the
 // states that the forward pass kept every 16 tokens: reading them costs 4/16
 // byte an element, reading h itself 2 to 4 and, in bf16, its rounding in dg.
-template <typename T, int V, int S, bool BETA, int LOAD>
-__global__ void __launch_bounds__(32 * kWarps, 4)
+template <typename T, int V, int S, int W, bool BETA, bool TMA>
+__global__ void __launch_bounds__(32 * W, 16 / W)
     scan_backward_kernel(const ScanBackwardArgs a, const __grid_constant__ ScanMaps maps) {
   // the later slices of a kept state's 16 tokens start from the slices before
   constexpr int M = kCarryTokens / S;
   extern __shared__ __align__(128) unsigned char smem[];
-  auto& ex = *reinterpret_cast<Exchange<V>*>(smem);
-  auto& fwd = *reinterpret_cast<Map<V>(*)[2][kWarps][32]>(smem + sizeof(Exchange<V>));
-  auto& st = *reinterpret_cast<Stage<T, V, S, BETA ? 3 : 2>*>(smem + sizeof(Exchange<V>) +
+  auto& ex = *reinterpret_cast<Exchange<V, W>*>(smem);
+  auto& fwd = *reinterpret_cast<Map<V>(*)[2][W][32]>(smem + sizeof(Exchange<V, W>));
+  auto& st = *reinterpret_cast<Stage<T, V, S, W, BETA ? 3 : 2>*>(smem + sizeof(Exchange<V, W>) +
                                                               sizeof(fwd));
   const ScanArgs& f = a.f;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
@@ -473,12 +442,12 @@ __global__ void __launch_bounds__(32 * kWarps, 4)
     if (f.status && threadIdx.x == 0 && rank == 0) *f.status = GDN_ERR_SHAPE;
     return;
   }
-  exchange_init(ex, n, LOAD == kTma);
+  exchange_init(ex, n, TMA);
   F<V> carry{};
   if (a.dh_T) carry = to_f(load<float, V>(a.dh_T + (size_t)seq * f.C + c0));
-  constexpr int tile = kWarps * S;
+  constexpr int tile = W * S;
   const int tiles = (s.len + tile - 1) / tile;
-  const int sw = kWarps - 1 - w;  // scan order runs backwards in time
+  const int sw = W - 1 - w;  // scan order runs backwards in time
   const size_t gs = size_t(f.C) * 4, ts = size_t(f.C) * sizeof(T);
   int ti = tiles - 1 - int(rank), cnt = 0;  // the tile; below 0: past the start
   const char *pg = nullptr, *pd = nullptr, *px = nullptr, *pb = nullptr;
@@ -494,14 +463,8 @@ __global__ void __launch_bounds__(32 * kWarps, 4)
     pd = reinterpret_cast<const char*>(static_cast<const T*>(a.dh) + at);
     px = reinterpret_cast<const char*>(static_cast<const T*>(f.x) + at);
     if (BETA) pb = reinterpret_cast<const char*>(static_cast<const T*>(f.beta) + at);
-    if constexpr (LOAD == kCopies) {
-      fetch(st.g[w], pg, gs, cnt);
-      fetch(st.t[0][w], pd, ts, cnt);
-      fetch(st.t[1][w], px, ts, cnt);
-      if constexpr (BETA) fetch(st.t[2][w], pb, ts, cnt);
-    }
-    if (LOAD == kTma && cnt > 0 && !late) ++issued;
-    if (LOAD == kTma && cnt > 0 && !late && lane == 0) {
+    if (TMA && cnt > 0 && !late) ++issued;
+    if (TMA && cnt > 0 && !late && lane == 0) {
       const int c = (id % f.cblocks) * 32 * V, row = int(s.start) + t0;
       bar_expect(&ex.full[w], sizeof(st.g[w]) + (BETA ? 3 : 2) * sizeof(st.t[0][w]));
       tma_rows(&st.g[w], &maps.g, &ex.full[w], c, row);
@@ -516,15 +479,14 @@ __global__ void __launch_bounds__(32 * kWarps, 4)
   int round = 0;
   for (int first = 0; first < tiles; first += int(n), ++round) {
     const int set = round & 1;
-    if (LOAD == kCopies) copies_done();
-    if (LOAD == kTma && cnt > 0) bar_wait(&ex.full[w], (issued - 1) & 1, &late);
+    if (TMA && cnt > 0) bar_wait(&ex.full[w], (issued - 1) & 1, &late);
     Vec<float, V> g[S];
     Vec<T, V> x[S], b[S], d[S];
-    take<LOAD>(g, st.g[w], pg, gs, cnt);
-    take<LOAD>(d, st.t[0][w], pd, ts, cnt);
-    take<LOAD>(x, st.t[1][w], px, ts, cnt);
-    if (BETA) take<LOAD>(b, st.t[BETA ? 2 : 0][w], pb, ts, cnt);
-    if (LOAD == kTma) __syncwarp();
+    take<TMA>(g, st.g[w], pg, gs, cnt);
+    take<TMA>(d, st.t[0][w], pd, ts, cnt);
+    take<TMA>(x, st.t[1][w], px, ts, cnt);
+    if (BETA) take<TMA>(b, st.t[BETA ? 2 : 0][w], pb, ts, cnt);
+    if (TMA) __syncwarp();
     F<V> h = to_f(kept), mu;
     const size_t out = at;
     const int have = cnt;
@@ -543,7 +505,7 @@ __global__ void __launch_bounds__(32 * kWarps, 4)
     for (int i = S - 1; i >= 0; --i) m.H = mul(al[i], add(to_f(d[i]), m.H));
     mf.A = m.A = finite(decay(m.A));
     if (M > 1) fwd[set][sw][lane] = mf;
-    scan_exchange<V>(ex, round, m, carry, mu, w, lane, rank, n, &late);
+    scan_exchange(ex, round, m, carry, mu, w, lane, rank, n, &late);
     if (M > 1) {
 #pragma unroll
       for (int i = 0; i < M - 1; ++i)
@@ -592,39 +554,60 @@ __global__ void __launch_bounds__(256) scan_step_kernel(const T* x, const float*
   store<T, V>(h + i, r);
 }
 
-// CTAs along time: as many, up to 8, as are all resident at once (four per SM),
-// as long as each has tokens of a sequence of average length.  4 x 4096 x 2048
-// (128 chains) forward: 88 us on 1 CTA, 62 on 2, 57 on 4, 61 on 8 (two waves).
-int pick_cluster(const ScanArgs& a, int S, long long chains, int sms) {
+// Warps of a CTA and CTAs of a cluster, both along time.  16 warps an SM are
+// resident at 128 registers.  In microseconds, forward / backward, at bf16 with beta:
+//   few     (one 16-token slice, or chains enough to fill the GPU one warp each)
+//           64 x 16 x 4096: 12 / 19 against 24 / 27 on four warps
+//   8, n=1  packed sequences, whose longest bound the launch: 32 of 512 tokens on
+//           average, 2048 channels, 51 / 107 against 56 / 134 on four warps;
+//           1.5 to 4 chains an SM: 8 x 2048 x 2048 56 / 111, four warps on two
+//           CTAs 59 / 126
+//   4, n    else as many CTAs as are resident at once: 4 x 4096 x 2048 86 / 190 on
+//           1, 62 / 137 on 2, 58 / 108 on 4, 62 / 112 on 8 (two waves)
+//   8, n=8  so few chains that even this is resident: 4096 x 2048 20 / 35 against
+//           21 / 42 on four warps
+// A tenth of what is resident is left free: clusters do not fill every GPC.
+struct Shape {
+  int warps, cluster;
+};
+Shape pick_shape(const ScanArgs& a, int S, long long chains, int sms, int few) {
   const long long len = a.cu_seqlens ? std::max<long long>(1, a.T / std::max(1, a.N)) : a.T;
+  if (len <= few * S || chains >= 16LL * sms) return {few, 1};
+  const auto resident = [&](int warps) { return 16 / warps * (long long)sms * 9 / 10; };
+  int W = 4;
+  if (len > 4 * S && (a.cu_seqlens || (2 * chains >= 3LL * sms && chains <= 4LL * sms) ||
+                      chains * kMaxCluster <= resident(8)))
+    W = 8;
   int n = 1;
-  while (n < kMaxCluster && chains * n * 2 <= 4LL * sms && (long long)n * kWarps * S < len) n *= 2;
-  return n;
+  while (n < kMaxCluster && chains * n * 2 <= resident(W) && (long long)n * W * S < len) n *= 2;
+  return {W, n};
 }
 
-// go(has beta, loader), both as types.
-template <typename T, int V, typename Go>
-bool dispatch_load(bool beta, bool tma, Go&& go) {
-  const auto with = [&](auto b) {
-    if constexpr (V == 1 && sizeof(T) == 2) {
-      return go(b, std::integral_constant<int, kDirect>{});
-    } else if constexpr (V == 2) {
-      return tma ? go(b, std::integral_constant<int, kTma>{})
-                 : go(b, std::integral_constant<int, kCopies>{});
-    } else {
-      return go(b, std::integral_constant<int, kCopies>{});
-    }
+// go(warps, has beta, by TMA), all as types.  Odd channel counts have four or eight
+// warps and no TMA.
+template <int V, int FEW, typename Go>
+bool dispatch_scan(int warps, bool beta, bool tma, Go&& go) {
+  const auto with = [&](auto w, auto b) {
+    if constexpr (V == 2)
+      if (tma) return go(w, b, std::true_type{});
+    return go(w, b, std::false_type{});
   };
-  return beta ? with(std::true_type{}) : with(std::false_type{});
+  const auto sized = [&](auto w) {
+    return beta ? with(w, std::true_type{}) : with(w, std::false_type{});
+  };
+  if constexpr (V == 2)
+    if (warps == FEW) return sized(std::integral_constant<int, FEW>{});
+  if (warps == 8) return sized(std::integral_constant<int, 8>{});
+  return sized(std::integral_constant<int, 4>{});
 }
 
 template <auto Kernel, typename Args>
-bool launch_cluster(const Args& args, const ScanMaps& maps, size_t smem, long long ctas, int n,
-                    cudaStream_t stream) {
+bool launch_cluster(const Args& args, const ScanMaps& maps, int threads, size_t smem,
+                    long long ctas, int n, cudaStream_t stream) {
   if (!raise_smem<Kernel>(smem)) return false;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(unsigned(ctas * n));
-  cfg.blockDim = dim3(32 * kWarps);
+  cfg.blockDim = dim3(unsigned(threads));
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute at{};
@@ -647,13 +630,23 @@ bool tma_ok(const ScanArgs& a, long long rows, int esize, std::initializer_list<
   return aligned(a.g, 16);
 }
 
+// The shape of a launch, its channel blocks and the order of its sequences.
+template <int V>
+bool plan(ScanArgs& a, int S, int few, int sms, long long* chains, Shape* shape) {
+  a.cblocks = (a.C + 32 * V - 1) / (32 * V);
+  *chains = (long long)a.cblocks * a.N;
+  if (*chains * kMaxCluster > 0x7fffffffLL) return false;
+  *shape = pick_shape(a, S, *chains, sms, V == 2 ? few : 4);
+  a.sorted = a.cu_seqlens && a.N <= kMaxSorted && shape->warps >= 4 &&
+             *chains * shape->cluster > 16 / shape->warps * (long long)sms;
+  return true;
+}
+
 template <typename T, int V, int S>
 int run_scan(ScanArgs a, int sms, cudaStream_t stream) {
-  a.cblocks = (a.C + 32 * V - 1) / (32 * V);
-  const long long chains = (long long)a.cblocks * a.N;
-  if (chains * kMaxCluster > 0x7fffffffLL) return GDN_ERR_SHAPE;
-  const int n = pick_cluster(a, S, chains, sms);
-  a.sorted = a.cu_seqlens && a.N <= kMaxSorted && chains * n > 4LL * sms;
+  long long chains;
+  Shape sh;
+  if (!plan<V>(a, S, 1, sms, &chains, &sh)) return GDN_ERR_SHAPE;
   const long long rows = a.cu_seqlens ? a.T : (long long)a.N * a.T;
   constexpr bool bf16 = sizeof(T) == 2;
   ScanMaps maps{};
@@ -662,25 +655,24 @@ int run_scan(ScanArgs a, int sms, cudaStream_t stream) {
     tma = encode_rows(&maps.g, a.g, rows, a.C, 64, S, false) &&
           encode_rows(&maps.t[0], a.x, rows, a.C, 64, S, bf16) &&
           (!a.beta || encode_rows(&maps.t[1], a.beta, rows, a.C, 64, S, bf16));
-  const auto go = [&](auto beta, auto load) {
-    constexpr bool kBeta = decltype(beta)::value;
-    constexpr int kLoad = decltype(load)::value;
+  const auto go = [&](auto warps, auto beta, auto by_tma) {
+    constexpr int W = decltype(warps)::value;
+    constexpr bool kBeta = decltype(beta)::value, kTma = decltype(by_tma)::value;
     constexpr size_t smem =
-        sizeof(Exchange<V>) + (kLoad != kDirect ? sizeof(Stage<T, V, S, kBeta ? 2 : 1>) : 0);
-    return launch_cluster<&scan_kernel<T, V, S, kBeta, kLoad>>(a, maps, smem, chains, n, stream);
+        sizeof(Exchange<V, W>) + (kTma ? sizeof(Stage<T, V, S, W, kBeta ? 2 : 1>) : 0);
+    return launch_cluster<&scan_kernel<T, V, S, W, kBeta, kTma>>(a, maps, 32 * W, smem, chains,
+                                                                  sh.cluster, stream);
   };
-  return dispatch_load<T, V>(a.beta != nullptr, tma, go) ? GDN_OK : GDN_ERR_LAUNCH;
+  return dispatch_scan<V, 1>(sh.warps, a.beta != nullptr, tma, go) ? GDN_OK : GDN_ERR_LAUNCH;
 }
 
 template <typename T, int V, int S>
 int run_backward(ScanBackwardArgs a, int sms, cudaStream_t stream) {
-  static_assert(kWarps * S % kCarryTokens == 0, "a tile starts at a kept state");
   ScanArgs& f = a.f;
-  f.cblocks = (f.C + 32 * V - 1) / (32 * V);
-  const long long chains = (long long)f.cblocks * f.N;
-  if (chains * kMaxCluster > 0x7fffffffLL) return GDN_ERR_SHAPE;
-  const int n = pick_cluster(f, S, chains, sms);
-  f.sorted = f.cu_seqlens && f.N <= kMaxSorted && chains * n > 4LL * sms;
+  long long chains;
+  Shape sh;
+  constexpr int kFew = kCarryTokens / S;  // a tile starts at a kept state
+  if (!plan<V>(f, S, kFew, sms, &chains, &sh)) return GDN_ERR_SHAPE;
   const long long rows = f.cu_seqlens ? f.T : (long long)f.N * f.T;
   constexpr bool bf16 = sizeof(T) == 2;
   ScanMaps maps{};
@@ -690,15 +682,15 @@ int run_backward(ScanBackwardArgs a, int sms, cudaStream_t stream) {
           encode_rows(&maps.t[0], a.dh, rows, f.C, 64, S, bf16) &&
           encode_rows(&maps.t[1], f.x, rows, f.C, 64, S, bf16) &&
           (!f.beta || encode_rows(&maps.t[2], f.beta, rows, f.C, 64, S, bf16));
-  const auto go = [&](auto beta, auto load) {
-    constexpr bool kBeta = decltype(beta)::value;
-    constexpr int kLoad = decltype(load)::value;
-    constexpr size_t smem = sizeof(Exchange<V>) + sizeof(Map<V>[2][kWarps][32]) +
-                            (kLoad != kDirect ? sizeof(Stage<T, V, S, kBeta ? 3 : 2>) : 0);
-    return launch_cluster<&scan_backward_kernel<T, V, S, kBeta, kLoad>>(a, maps, smem, chains, n,
-                                                                        stream);
+  const auto go = [&](auto warps, auto beta, auto by_tma) {
+    constexpr int W = decltype(warps)::value;
+    constexpr bool kBeta = decltype(beta)::value, kTma = decltype(by_tma)::value;
+    constexpr size_t smem = sizeof(Exchange<V, W>) + sizeof(Map<V>[2][W][32]) +
+                            (kTma ? sizeof(Stage<T, V, S, W, kBeta ? 3 : 2>) : 0);
+    return launch_cluster<&scan_backward_kernel<T, V, S, W, kBeta, kTma>>(
+        a, maps, 32 * W, smem, chains, sh.cluster, stream);
   };
-  return dispatch_load<T, V>(f.beta != nullptr, tma, go) ? GDN_OK : GDN_ERR_LAUNCH;
+  return dispatch_scan<V, kFew>(sh.warps, f.beta != nullptr, tma, go) ? GDN_OK : GDN_ERR_LAUNCH;
 }
 
 // Two channels a thread where the channel count is even and every array starts
