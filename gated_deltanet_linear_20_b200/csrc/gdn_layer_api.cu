@@ -127,9 +127,9 @@ size_t gdn_scan_carry_bytes(int N, int tokens, int C, int packed) {
 }
 
 int gdn_scan(const void* x, const float* g, const void* beta, const float* h0, void* h, float* h_T,
-             float* carries, int B, int T, int C, int dtype, void* stream) {
+             float* carries, int B, int T, int C, int dtype, int* status, void* stream) {
   if (B < 0 || T < 0) return GDN_ERR_SHAPE;
-  return scan_impl({x, g, beta, h0, h, h_T, carries, nullptr, B, T, C, 0, nullptr},
+  return scan_impl({x, g, beta, h0, h, h_T, carries, nullptr, B, T, C, 0, status},
                    (long long)B * T, dtype, stream);
 }
 
@@ -164,10 +164,10 @@ int gdn_scan_step(const void* x, const float* g, const void* beta, float* state,
 int gdn_scan_backward(const void* x, const float* g, const void* beta, const float* h0,
                       const void* dh, const float* dh_T, void* dx, float* dg, void* dbeta,
                       float* dh0, float* carries, int carries_valid, int B, int T, int C,
-                      int dtype, void* stream) {
+                      int dtype, int* status, void* stream) {
   if (B < 0 || T < 0) return GDN_ERR_SHAPE;
   return scan_backward_impl(
-      {{x, g, beta, h0, nullptr, nullptr, carries, nullptr, B, T, C, 0, nullptr}, dh, dh_T, dx, dg,
+      {{x, g, beta, h0, nullptr, nullptr, carries, nullptr, B, T, C, 0, status}, dh, dh_T, dx, dg,
        dbeta, dh0},
       carries_valid, (long long)B * T, dtype, stream);
 }

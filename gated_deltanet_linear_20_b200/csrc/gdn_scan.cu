@@ -36,9 +36,11 @@
 namespace gdn {
 namespace {
 
+using namespace sm100;
+
 constexpr int kCarryTokens = GDN_SCAN_CARRY_TOKENS;
 constexpr int kMaxCluster = 8;  // CTAs along time
-constexpr uint64_t kWaitLimitNs = 2000000000;  // of a wait for the cluster's maps
+constexpr uint64_t kWaitLimitNs = 2000000000;  // 2 s: far beyond any legitimate wait
 constexpr long long kTmaElements = 1 << 17;  // of a call, from which TMA is used
 constexpr int kMaxSorted = 128;  // packed sequences that are started longest first
 
@@ -95,10 +97,10 @@ __device__ __forceinline__ void store_remote(Map<V>* local, uint64_t* bar, unsig
   unsigned a, b;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
                : "=r"(a)
-               : "r"(static_cast<unsigned>(__cvta_generic_to_shared(local))), "r"(rank));
+               : "r"(smem_u32(local)), "r"(rank));
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
                : "=r"(b)
-               : "r"(static_cast<unsigned>(__cvta_generic_to_shared(bar))), "r"(rank));
+               : "r"(smem_u32(bar)), "r"(rank));
   if constexpr (V == 2)
     asm volatile(
         "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%2, %3, %4, %5}, "
@@ -112,38 +114,6 @@ __device__ __forceinline__ void store_remote(Map<V>* local, uint64_t* bar, unsig
         "r"(b), "f"(m.A.v[0]), "f"(m.H.v[0])
         : "memory");
 }
-__device__ __forceinline__ void bar_expect(uint64_t* bar, unsigned bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(
-                   static_cast<unsigned>(__cvta_generic_to_shared(bar))),
-               "r"(bytes)
-               : "memory");
-}
-__device__ __forceinline__ bool bar_ready(uint64_t* bar, unsigned parity) {
-  unsigned ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}\n"
-      : "=r"(ok)
-      : "r"(static_cast<unsigned>(__cvta_generic_to_shared(bar))), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
-// Waits for the phase, or gives up after the limit (*late, alike in all lanes;
-// nothing is awaited then).
-__device__ __forceinline__ void bar_wait(uint64_t* bar, unsigned parity, bool* late) {
-  if (*late || __all_sync(0xffffffffu, bar_ready(bar, parity))) return;
-  const uint64_t begin = sm100::globaltimer_ns();
-  unsigned polls = 0;
-  while (!__all_sync(0xffffffffu, bar_ready(bar, parity)))
-    if ((++polls & 255u) == 0 &&
-        __any_sync(0xffffffffu, sm100::globaltimer_ns() - begin > kWaitLimitNs)) {
-      *late = true;
-      return;
-    }
-}
-
 struct Seq {
   long long start;  // first token
   int len;
@@ -200,16 +170,11 @@ template <int V, int W>
 __device__ __forceinline__ void exchange_init(Exchange<V, W>& ex, unsigned n, bool tma) {
   if (n == 1 && !tma) return;
   if (threadIdx.x == 0) {
-    const auto init = [](uint64_t* bar) {
-      asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(
-                       static_cast<unsigned>(__cvta_generic_to_shared(bar)))
-                   : "memory");
-    };
-    init(&ex.bar[0]);
-    init(&ex.bar[1]);
+    mbar_init(smem_u32(&ex.bar[0]), 1);
+    mbar_init(smem_u32(&ex.bar[1]), 1);
 #pragma unroll
-    for (int i = 0; i < W; ++i) init(&ex.full[i]);
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    for (int i = 0; i < W; ++i) mbar_init(smem_u32(&ex.full[i]), 1);
+    fence_mbar_init();
   }
   if (n > 1)
     cluster_barrier();  // every CTA runs, its barriers ready, before it is written to
@@ -230,7 +195,7 @@ __device__ __forceinline__ void scan_exchange(Exchange<V, W>& ex, int round, con
                                               unsigned rank, unsigned n, bool* late) {
   const int set = round & 1;
   ex.warp[set][w][lane] = mine;
-  if (n > 1 && threadIdx.x == 0 && !*late) bar_expect(&ex.bar[set], n * 32 * sizeof(Map<V>));
+  if (n > 1 && threadIdx.x == 0 && !*late) mbar_arrive_expect_tx(smem_u32(&ex.bar[set]), n * 32 * sizeof(Map<V>));
   __syncthreads();
   c = carry;
   if (n > 1) {
@@ -245,7 +210,7 @@ __device__ __forceinline__ void scan_exchange(Exchange<V, W>& ex, int round, con
       for (unsigned r = w; r < n; r += W)
         store_remote(&ex.cta[set][rank][lane], &ex.bar[set], r, m);
     }
-    bar_wait(&ex.bar[set], (round >> 1) & 1, late);
+    mbar_wait_warp(smem_u32(&ex.bar[set]), (round >> 1) & 1, late, kWaitLimitNs);
     for (unsigned r = 0; r < n; ++r) {
       if (r == rank) c = carry;
       carry = apply(ex.cta[set][r][lane], carry);
@@ -269,7 +234,7 @@ __device__ __forceinline__ void exchange_end(unsigned n, bool late, int* status,
   if (late) {
     if (status) *status = GDN_ERR_DEVICE_TIMEOUT;
     bool again = false;
-    if (issued > 0) bar_wait(full, (issued - 1) & 1, &again);
+    if (issued > 0) mbar_wait_warp(smem_u32(full), (issued - 1) & 1, &again, kWaitLimitNs);
   }
   if (n > 1) cluster_barrier();
 }
@@ -295,9 +260,9 @@ __device__ __forceinline__ void tma_rows(void* dst, const CUtensorMap* map, uint
                                          int row) {
   asm volatile(
       "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4}], [%2];" ::"r"(static_cast<unsigned>(__cvta_generic_to_shared(dst))),
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
       "l"(reinterpret_cast<uint64_t>(map)),
-      "r"(static_cast<unsigned>(__cvta_generic_to_shared(bar))), "r"(c), "r"(row)
+      "r"(smem_u32(bar)), "r"(c), "r"(row)
       : "memory");
 }
 
@@ -362,7 +327,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W)
     if (TMA && cnt > 0 && !late) ++issued;
     if (TMA && cnt > 0 && !late && lane == 0) {
       const int c = (id % a.cblocks) * 32 * V, row = int(s.start) + t0;
-      bar_expect(&ex.full[w], sizeof(st.g[w]) + (BETA ? 2 : 1) * sizeof(st.t[0][w]));
+      mbar_arrive_expect_tx(smem_u32(&ex.full[w]), sizeof(st.g[w]) + (BETA ? 2 : 1) * sizeof(st.t[0][w]));
       tma_rows(&st.g[w], &maps.g, &ex.full[w], c, row);
       tma_rows(&st.t[0][w], &maps.t[0], &ex.full[w], c, row);
       if (BETA) tma_rows(&st.t[BETA ? 1 : 0][w], &maps.t[1], &ex.full[w], c, row);
@@ -371,7 +336,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W)
   if (s.len > 0) place();
   int round = 0;
   for (int base = 0; base < s.len; base += step, ++round) {
-    if (TMA && cnt > 0) bar_wait(&ex.full[w], (issued - 1) & 1, &late);
+    if (TMA && cnt > 0) mbar_wait_warp(smem_u32(&ex.full[w]), (issued - 1) & 1, &late, kWaitLimitNs);
     Vec<float, V> g[S];
     Vec<T, V> x[S], b[S];
     take<TMA>(g, st.g[w], pg, gs, cnt);
@@ -466,7 +431,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W)
     if (TMA && cnt > 0 && !late) ++issued;
     if (TMA && cnt > 0 && !late && lane == 0) {
       const int c = (id % f.cblocks) * 32 * V, row = int(s.start) + t0;
-      bar_expect(&ex.full[w], sizeof(st.g[w]) + (BETA ? 3 : 2) * sizeof(st.t[0][w]));
+      mbar_arrive_expect_tx(smem_u32(&ex.full[w]), sizeof(st.g[w]) + (BETA ? 3 : 2) * sizeof(st.t[0][w]));
       tma_rows(&st.g[w], &maps.g, &ex.full[w], c, row);
       tma_rows(&st.t[0][w], &maps.t[0], &ex.full[w], c, row);
       tma_rows(&st.t[1][w], &maps.t[1], &ex.full[w], c, row);
@@ -479,7 +444,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W)
   int round = 0;
   for (int first = 0; first < tiles; first += int(n), ++round) {
     const int set = round & 1;
-    if (TMA && cnt > 0) bar_wait(&ex.full[w], (issued - 1) & 1, &late);
+    if (TMA && cnt > 0) mbar_wait_warp(smem_u32(&ex.full[w]), (issued - 1) & 1, &late, kWaitLimitNs);
     Vec<float, V> g[S];
     Vec<T, V> x[S], b[S], d[S];
     take<TMA>(g, st.g[w], pg, gs, cnt);

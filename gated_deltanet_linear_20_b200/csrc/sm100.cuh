@@ -60,6 +60,31 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity,
   }
 }
 
+// mbar_try_wait that also acquires what other CTAs of the cluster stored (st.async).
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// A whole warp waits for the phase, or gives up after `limit_ns`: *late becomes
+// true, alike in all lanes, and nothing is awaited from then on.
+__device__ __forceinline__ void mbar_wait_warp(uint32_t bar, uint32_t parity, bool* late,
+                                               uint64_t limit_ns) {
+  if (*late || __all_sync(0xffffffffu, mbar_try_wait_cluster(bar, parity))) return;
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t it = 1; !__all_sync(0xffffffffu, mbar_try_wait_cluster(bar, parity)); ++it)
+    if ((it & 255u) == 0u && __any_sync(0xffffffffu, globaltimer_ns() - t0 > limit_ns)) {
+      *late = true;
+      return;
+    }
+}
+
 // Plain arrive (count 1) on an mbarrier, release semantics at CTA scope.
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");

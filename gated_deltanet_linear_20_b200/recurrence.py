@@ -17,10 +17,10 @@ import torch
 from .gdn import GDN_OK, GDNError, _check, _lib
 
 _vp, _ci = ctypes.c_void_p, ctypes.c_int
-for _name, _args in (("gdn_scan", [_vp] * 7 + [_ci] * 4 + [_vp]),
+for _name, _args in (("gdn_scan", [_vp] * 7 + [_ci] * 4 + [_vp, _vp]),
                      ("gdn_scan_varlen", [_vp] * 8 + [_ci] * 4 + [_vp, _vp]),
                      ("gdn_scan_step", [_vp] * 5 + [_ci] * 3 + [_vp]),
-                     ("gdn_scan_backward", [_vp] * 11 + [_ci] * 5 + [_vp]),
+                     ("gdn_scan_backward", [_vp] * 11 + [_ci] * 5 + [_vp, _vp]),
                      ("gdn_scan_varlen_backward", [_vp] * 11 + [_ci, _vp] + [_ci] * 4 + [_vp, _vp])):
     getattr(_lib, _name).argtypes = _args
     getattr(_lib, _name).restype = _ci
@@ -94,7 +94,8 @@ def _carry_shape(N: int, tokens: int, C: int, packed: bool):
 
 def scan(x: torch.Tensor, g: torch.Tensor, beta: Optional[torch.Tensor] = None,
          h0: Optional[torch.Tensor] = None, *, h: Optional[torch.Tensor] = None,
-         h_T: Optional[torch.Tensor] = None, save_carries: bool = False):
+         h_T: Optional[torch.Tensor] = None, save_carries: bool = False,
+         status: Optional[torch.Tensor] = None):
     """The recurrence over B sequences of T tokens: returns (h [B,T,C], h_T [B,C] fp32).
 
     x, beta [B,T,C] fp32 or bf16 (beta None: 1); g [B,T,C] fp32 natural-log
@@ -112,12 +113,13 @@ def scan(x: torch.Tensor, g: torch.Tensor, beta: Optional[torch.Tensor] = None,
     pg = _expect(g, "g", _F32, shape, dev)
     pb = _optional(beta, "beta", x.dtype, shape, dev)
     p0 = _optional(h0, "h0", _F32, (B, C), dev)
+    pst = _optional(status, "status", _I32, (1,), dev)
     h = _out(h, "h", x.dtype, shape, dev, x)
     h_T = _out(h_T, "h_T", _F32, (B, C), dev)
     carries = torch.empty(_carry_shape(B, B * T, C, False), dtype=_F32, device=dev) \
         if save_carries else None
     _call(_lib.gdn_scan, dev, px, pg, pb, p0, h.data_ptr(), h_T.data_ptr(),
-          None if carries is None else carries.data_ptr(), B, T, C, dt)
+          None if carries is None else carries.data_ptr(), B, T, C, dt, pst)
     return (h, h_T, carries) if save_carries else (h, h_T)
 
 
@@ -202,7 +204,8 @@ def _backward(fn, dh, x, g, beta, h0, dh_T, carries, N, tokens, packed, sizes,
 
 def scan_backward(dh: torch.Tensor, x: torch.Tensor, g: torch.Tensor,
                   beta: Optional[torch.Tensor] = None, h0: Optional[torch.Tensor] = None,
-                  dh_T: Optional[torch.Tensor] = None, *, carries: Optional[torch.Tensor] = None):
+                  dh_T: Optional[torch.Tensor] = None, *, carries: Optional[torch.Tensor] = None,
+                  status: Optional[torch.Tensor] = None):
     """Gradients of ``scan``'s inputs: returns (dx, dg, dbeta, dh0), dbeta and dh0
     None where beta and h0 are.
 
@@ -213,8 +216,9 @@ def scan_backward(dh: torch.Tensor, x: torch.Tensor, g: torch.Tensor,
     if x.dim() != 3:
         raise ValueError("x must be [B,T,C]")
     B, T, _ = x.shape
+    pst = _optional(status, "status", _I32, (1,), dev)
     return _backward(_lib.gdn_scan_backward, dh, x, g, beta, h0, dh_T, carries, B, B * T, False,
-                     (B, T), (), dev)
+                     (B, T), (pst,), dev)
 
 
 def scan_varlen_backward(dh: torch.Tensor, x: torch.Tensor, g: torch.Tensor,

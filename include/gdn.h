@@ -401,6 +401,8 @@ enum gdn_dtype { GDN_F32 = 0, GDN_BF16 = 1 };
  * are walked in parallel and joined exactly up to rounding, as long as the
  * growth exp(sum of g) over 1024 consecutive tokens stays in the fp32 range.
  * Results do not depend on timing (bitwise repeatable on the same device).
+ * status: optional device int, as for gdn_prefill: a bounded device wait that
+ * gives up stores GDN_ERR_DEVICE_TIMEOUT there.
  * B*C == 0 is a no-op; T == 0 writes h_T = h0 (or zeros).  Arrays need the
  * alignment of their element type; offsets are 64-bit: B*T up to 2^30 tokens.
  * Returns GDN_OK after enqueueing, GDN_ERR_NULL, GDN_ERR_ALIGN, GDN_ERR_SHAPE
@@ -408,7 +410,7 @@ enum gdn_dtype { GDN_F32 = 0, GDN_BF16 = 1 };
  * (an output overlaps an input or another output, except h_T == h0) or
  * GDN_ERR_LAUNCH. */
 int gdn_scan(const void* x, const float* g, const void* beta, const float* h0, void* h, float* h_T,
-             float* carries, int B, int T, int C, int dtype, void* stream);
+             float* carries, int B, int T, int C, int dtype, int* status, void* stream);
 
 /* gdn_scan of N sequences packed along the token axis, as in
  * gdn_prefill_varlen: x, g, beta, h [total_T][C], h0, h_T [N][C], cu_seqlens
@@ -446,11 +448,11 @@ int gdn_scan_step(const void* x, const float* g, const void* beta, float* state,
  *              launch that reads x, g and beta once more).  Two calls in flight
  *              must not share scratch.
  * Sums and states are fp32; h is rebuilt in fp32, not read back rounded.
- * Sizes, alignment, errors and repeatability as for gdn_scan. */
+ * Sizes, alignment, status, errors and repeatability as for gdn_scan. */
 int gdn_scan_backward(const void* x, const float* g, const void* beta, const float* h0,
                       const void* dh, const float* dh_T, void* dx, float* dg, void* dbeta,
                       float* dh0, float* carries, int carries_valid, int B, int T, int C,
-                      int dtype, void* stream);
+                      int dtype, int* status, void* stream);
 
 /* gdn_scan_backward of packed sequences (gdn_scan_varlen).  An invalid
  * sequence's gradients are not written. */

@@ -58,7 +58,7 @@ MB = 1 << 24
 
 def scan_args(**over):
     a = dict(x=P, g=P + MB, beta=P + 2 * MB, h0=P + 3 * MB, h=P + 4 * MB, h_T=P + 5 * MB,
-             carries=P + 6 * MB, B=2, T=40, C=64, dtype=1, stream=None)
+             carries=P + 6 * MB, B=2, T=40, C=64, dtype=1, status=None, stream=None)
     a.update(over)
     return list(a.values())
 
@@ -75,6 +75,7 @@ def scan_args(**over):
     (dict(h=P), -5), (dict(h=P + MB + 64), -5), (dict(h_T=P + 2 * MB), -5),
     (dict(h_T=P + 3 * MB + 4), -5),                         # partly over h0
     (dict(h=P + 3 * MB), -5), (dict(h=P + 5 * MB), -5), (dict(carries=P + 4 * MB + 4), -5),
+    (dict(status=P + 7 * MB + 1), -2), (dict(status=P + 4 * MB), -5),
 ], ids=str)
 def test_scan_refuses(lib, over, code):
     assert lib.gdn_scan(*scan_args(**over)) == code
@@ -117,7 +118,7 @@ def test_scan_step_refuses(lib, over, code):
 def backward_args(**over):
     a = dict(x=P, g=P + MB, beta=P + 2 * MB, h0=P + 3 * MB, dh=P + 4 * MB, dh_T=P + 5 * MB,
              dx=P + 6 * MB, dg=P + 7 * MB, dbeta=P + 8 * MB, dh0=P + 9 * MB, carries=P + 10 * MB,
-             valid=1, B=2, T=40, C=64, dtype=1, stream=None)
+             valid=1, B=2, T=40, C=64, dtype=1, status=None, stream=None)
     a.update(over)
     return list(a.values())
 
@@ -129,7 +130,7 @@ def backward_args(**over):
     (dict(dx=P + 6 * MB + 1), -2), (dict(dg=P + 7 * MB + 2), -2), (dict(dh_T=P + 5 * MB + 2), -2),
     (dict(dx=P + 4 * MB), -5), (dict(dg=P + MB), -5), (dict(dbeta=P + 2 * MB), -5),
     (dict(dh0=P + 3 * MB), -5), (dict(dh0=P + 5 * MB + 4), -5), (dict(dx=P + 8 * MB), -5),
-    (dict(carries=P), -5),
+    (dict(carries=P), -5), (dict(status=P + 6 * MB), -5),
 ], ids=str)
 def test_scan_backward_refuses(lib, over, code):
     assert lib.gdn_scan_backward(*backward_args(**over)) == code
