@@ -1,6 +1,8 @@
 // Internal declarations shared by the C-ABI layer and the kernel files.
 #pragma once
 
+#include <algorithm>
+
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
@@ -203,13 +205,12 @@ int launch_scan_backward(const ScanBackwardArgs& a, int dtype, int sms, cudaStre
 int launch_scan_step(const ScanArgs& a, int dtype, cudaStream_t stream);
 
 // The most CTAs of a norm's backward launch: each leaves one partial sum of each
-// weight gradient.  Two of 256 or one of 512 threads per SM of a B200, which is
-// what is resident at a time: fewer leave memory idle (131072 x 128: 53 us with
-// four per SM, 46 with two; 4096 x 4096: 83 with two, 76 with one).
+// weight gradient.  1024 threads per SM of a B200, at 8 channels a thread.
 constexpr int kNormMaxD = 16384;
 inline int norm_max_parts(long long rows, int D) {
-  const long long most = D <= 2048 ? 296 : 148;
-  return int(rows < most ? rows : most);
+  const int threads = D <= 256 ? 256 : (D + 255) / 256 * 32;
+  const long long most = 148 * std::max(1, 1024 / threads);
+  return int(std::min(rows, most));
 }
 
 // Norms: GDN_OK or a negative code; types GDN_F32 or GDN_BF16.

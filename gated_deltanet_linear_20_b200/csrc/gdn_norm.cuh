@@ -1,18 +1,18 @@
 // What the norm kernels share: the layout of a row over threads, its sums, the
 // gate, and the copies of the next rows.
 //
-// A row of D channels is held in registers by TPR threads, NV vectors of V
-// channels each (vector j of thread t: channels (j TPR + t) V ..), so it is read
-// from memory once, whatever is summed over it.  Short rows (TPR 8, 16, 32)
-// share a CTA of TH threads and sum by shuffles; longer ones have a CTA
-// (TPR == TH).
+// A row of D channels is held by TPR threads, NV vectors of V channels each
+// (vector j of thread t: channels (j TPR + t) V ..), so it is read from memory
+// once, whatever is summed over it.  Short rows (TPR 8, 16, 32) share a CTA and
+// sum by shuffles; longer ones have a CTA of as many warps as they need (TPR 0).
 //
 // CTAs are persistent, and each thread copies its part of the next rows to shared
 // memory asynchronously (a ring of two or three stages) while it works on the
 // present one: the sums over a row and their barriers would leave the memory
 // idle otherwise.  A thread reads only what it copied, so the ring needs no
-// barrier.  What is left is the instruction count, so that all sizes of a layout
-// are constants and channels are worked on in pairs.
+// barrier.  (One bulk copy an array and row, by one thread, was slower: 524288 x
+// 128 82 us against 67, 8192 x 4096 48 against 47.)  What is left is the
+// instruction count, so that channels are worked on in pairs.
 #pragma once
 
 #include <algorithm>
@@ -23,40 +23,56 @@
 
 namespace gdn {
 
+// TH: threads of a CTA, the most of them where TPR is 0.
 template <int TPR_, int TH_, int NV_, int V_>
 struct Layout {
   static constexpr int TPR = TPR_, TH = TH_, NV = NV_, V = V_;
-  static constexpr bool kShort = TPR <= 32;   // several rows a CTA
-  static constexpr int kRows = TH / TPR;
-  static constexpr int P = V >= 2 ? 2 : 1;    // channels worked on together
-  static constexpr int N = NV * V / P;        // such groups of a thread
-  // cp.async moves at least 4 bytes, and longer rows would not fit the ring
-  static constexpr bool kStaged = V == 4 && NV * TH <= 1024;
+  static constexpr bool kShort = TPR > 0;               // several rows a CTA
+  static constexpr int kRows = kShort ? TH / (TPR > 0 ? TPR : 1) : 1;
+  static constexpr int P = V >= 2 ? 2 : 1;              // channels worked on together
+  static constexpr int G = V / P, N = NV * G;           // such groups of a vector, a thread
+  static constexpr int kMost = (kShort ? TPR : TH) * NV * V;  // channels
 };
 
-// Stages of a ring whose arrays have `bytes` a channel in all: three, if the
-// longest staged row leaves room for them.
-constexpr int stages(size_t bytes) { return bytes * 4096 * 3 <= 220 * 1024 ? 3 : 2; }
+// Stages of a ring whose arrays have `bytes` a channel in all: three, or two, or
+// none where the longest row leaves no room (or copies, of 4 bytes at least and
+// slow below 8, are no help).
 template <typename L>
-constexpr size_t ring_bytes(size_t bytes) {
-  return L::kStaged ? stages(bytes) * bytes * L::TH * L::NV * L::V : 0;
+constexpr int stages(size_t bytes) {
+  const size_t fit = 220 * 1024 / (bytes * L::TH * L::NV * L::V);
+  return L::V != 4 || fit < 2 ? 0 : fit < 3 ? 2 : 3;
+}
+// Threads of a CTA for rows of D channels.
+template <typename L>
+int norm_threads(int D) {
+  return L::kShort ? L::TH : (D + L::NV * L::V * 32 - 1) / (L::NV * L::V * 32) * 32;
 }
 
-// This thread's place: the channel of its vector j is t V + j TPR V.
+// This thread's place: its row among the CTA's, the first channel of its vectors.
 template <typename L>
 struct Place {
-  int sub;          // its row among the CTA's
-  unsigned c0, D;   // its first channel, the row's channels
+  int sub;
+  unsigned c0, step, D;
   __device__ __forceinline__ explicit Place(int d)
-      : sub(L::kShort ? threadIdx.x / L::TPR : 0), c0((threadIdx.x % L::TPR) * L::V), D(d) {}
-  __device__ __forceinline__ bool has(int j) const { return c0 + j * L::TPR * L::V < D; }
+      : sub(L::kShort ? threadIdx.x / (L::kShort ? L::TPR : 1) : 0),
+        c0((L::kShort ? threadIdx.x % (L::kShort ? L::TPR : 1) : threadIdx.x) * L::V),
+        step((L::kShort ? L::TPR : blockDim.x) * L::V), D(d) {}
+  __device__ __forceinline__ unsigned channel(int j) const { return c0 + j * step; }
+  __device__ __forceinline__ bool has(int j) const { return channel(j) < D; }
 };
 
-// The channels of vector j among a thread's groups.
+// The channels of a vector, in groups.
 template <typename L, typename T>
-__device__ __forceinline__ void spread(F<L::P> (&r)[L::N], const Vec<T, L::V>& x, int j) {
+__device__ __forceinline__ void spread(F<L::P> (&r)[L::G], const Vec<T, L::V>& x) {
 #pragma unroll
-  for (int e = 0; e < L::V; ++e) r[(j * L::V + e) / L::P].v[e % L::P] = to_f(x.v[e]);
+  for (int e = 0; e < L::V; ++e) r[e / L::P].v[e % L::P] = to_f(x.v[e]);
+}
+template <typename L, typename T>
+__device__ __forceinline__ void store_vector(T* p, const F<L::P> (&r)[L::G]) {
+  float x[L::V];
+#pragma unroll
+  for (int e = 0; e < L::V; ++e) x[e] = r[e / L::P].v[e % L::P];
+  store<T, L::V>(p, x);
 }
 
 // One input array in the ring: BEFORE bytes a channel of other arrays lie before
@@ -64,15 +80,16 @@ __device__ __forceinline__ void spread(F<L::P> (&r)[L::N], const Vec<T, L::V>& x
 template <typename L, typename T, int BEFORE, int ALL>
 struct Ring {
   using E = Vec<T, L::V>;
-  static constexpr int kCh = L::TH * L::NV * L::V;
+  static constexpr int kStages = stages<L>(ALL);
   __device__ __forceinline__ static E* slot(unsigned char* smem, int stage, int j) {
-    return reinterpret_cast<E*>(smem + stage * (ALL * kCh) + BEFORE * kCh) + j * L::TH +
-           threadIdx.x;
+    const unsigned threads = L::kShort ? L::TH : blockDim.x;
+    return reinterpret_cast<E*>(smem + (stage * ALL + BEFORE) * (threads * L::NV * L::V)) +
+           j * threads + threadIdx.x;
   }
   // Channels past D stay zero in every stage.
   __device__ __forceinline__ static void clear(unsigned char* smem, const Place<L>& at) {
 #pragma unroll
-    for (int s = 0; s < stages(ALL); ++s)
+    for (int s = 0; s < kStages; ++s)
 #pragma unroll
       for (int j = 0; j < L::NV; ++j)
         if (!at.has(j)) *slot(smem, s, j) = E{};
@@ -83,16 +100,23 @@ struct Ring {
 #pragma unroll
     for (int j = 0; j < L::NV; ++j)
       if (at.has(j)) {
-        const E* src = reinterpret_cast<const E*>(p + (at.c0 + j * L::TPR * L::V));
+        const E* src = reinterpret_cast<const E*>(p + at.channel(j));
         if (L::kShort)
           copy_async(slot(smem, stage, j), src, on ? int(sizeof(E)) : 0);
         else
           copy_async(slot(smem, stage, j), src);
       }
   }
-  __device__ __forceinline__ static void take(F<L::P> (&r)[L::N], unsigned char* smem, int stage) {
-#pragma unroll
-    for (int j = 0; j < L::NV; ++j) spread<L, T>(r, *slot(smem, stage, j), j);
+  // Vector j of the present row: from the ring, or (no stages) from memory.
+  __device__ __forceinline__ static void take(F<L::P> (&r)[L::G], unsigned char* smem, int stage,
+                                              const T* p, int j, const Place<L>& at, bool on) {
+    if constexpr (kStages > 0) {
+      spread<L, T>(r, *slot(smem, stage, j));
+    } else {
+      E x{};
+      if (on && at.has(j)) x = load<T, L::V>(p + at.channel(j));
+      spread<L, T>(r, x);
+    }
   }
 };
 
@@ -102,43 +126,17 @@ __device__ __forceinline__ void copies_wait() {  // for the oldest stage in flig
   asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
 }
 
-// A row straight from memory (layouts that are not staged).
-template <typename L, typename T>
-__device__ __forceinline__ void load_row(F<L::P> (&r)[L::N], const T* p, const Place<L>& at,
-                                         bool on) {
-#pragma unroll
-  for (int j = 0; j < L::NV; ++j) {
-    Vec<T, L::V> x{};
-    if (on && at.has(j)) x = load<T, L::V>(p + (at.c0 + j * L::TPR * L::V));
-    spread<L, T>(r, x, j);
-  }
-}
-
-template <typename L, typename T>
-__device__ __forceinline__ void store_row(T* p, const F<L::P> (&r)[L::N], const Place<L>& at,
-                                          bool on) {
-#pragma unroll
-  for (int j = 0; j < L::NV; ++j)
-    if (on && at.has(j)) {
-      float x[L::V];
-#pragma unroll
-      for (int e = 0; e < L::V; ++e) x[e] = r[(j * L::V + e) / L::P].v[e % L::P];
-      store<T, L::V>(p + (at.c0 + j * L::TPR * L::V), x);
-    }
-}
-
-// The weights of this thread's channels, `offset` added; ones without any.
+// The weights of vector j, `offset` added; ones without any, zeros past D.
 template <typename L>
-__device__ __forceinline__ void load_weight(F<L::P> (&w)[L::N], const float* p, float offset,
+__device__ __forceinline__ void load_weight(F<L::P> (&w)[L::G], const float* p, float offset, int j,
                                             const Place<L>& at) {
-  if (!p) {
 #pragma unroll
-    for (int i = 0; i < L::N; ++i) w[i] = all<L::P>(1.f);
-    return;
+  for (int i = 0; i < L::G; ++i) w[i] = all<L::P>(p ? 0.f : 1.f);
+  if (p && at.has(j)) {
+    spread<L, float>(w, load<float, L::V>(p + at.channel(j)));
+#pragma unroll
+    for (int i = 0; i < L::G; ++i) w[i] = add(w[i], all<L::P>(offset));
   }
-  load_row<L, float>(w, p, at, true);
-#pragma unroll
-  for (int i = 0; i < L::N; ++i) w[i] = add(w[i], all<L::P>(offset));
 }
 
 template <int P>
@@ -147,16 +145,23 @@ __device__ __forceinline__ float total(F<P> a) {
 }
 
 // Sums of K values over the threads of a row; every thread gets them.  For rows
-// of several warps `buf` holds two sets, used in turn, so that one barrier a sum
-// is enough.  The order of the additions is fixed.
+// of a CTA `buf` holds two sets, used in turn, so that one barrier a sum is
+// enough.  The order of the additions is fixed.
 template <typename L, int K>
 struct SumBuffer {
-  static constexpr int kWarps = L::TH / 32;
-  float part[2][K == 1 ? 1 : 4][kWarps];
+  float part[2][K == 1 ? 1 : 4][16];
 };
+// Before the first sum (the places of warps that there are not stay zero).
+template <typename L, int K>
+__device__ __forceinline__ void sum_init(SumBuffer<L, K>& buf) {
+  if constexpr (!L::kShort) {
+    for (int i = threadIdx.x; i < 2 * (K == 1 ? 1 : 4) * 16; i += blockDim.x)
+      (&buf.part[0][0][0])[i] = 0.f;
+    __syncthreads();
+  }
+}
 template <typename L, int K>
 __device__ __forceinline__ void row_sum(float (&v)[K], SumBuffer<L, K>& buf, int& turn) {
-  constexpr int n = L::TH / 32;
   const auto halve = [](float x, int o) { return x + __shfl_xor_sync(0xffffffffu, x, o); };
   if constexpr (L::kShort || K == 1) {
     constexpr int W = L::kShort ? L::TPR : 32;
@@ -168,9 +173,9 @@ __device__ __forceinline__ void row_sum(float (&v)[K], SumBuffer<L, K>& buf, int
       const int lane = threadIdx.x & 31;
       if (lane == 0) buf.part[turn][0][threadIdx.x >> 5] = v[0];
       __syncthreads();
-      v[0] = buf.part[turn][0][lane % n];
+      v[0] = buf.part[turn][0][lane & 15];
 #pragma unroll
-      for (int o = n / 2; o > 0; o >>= 1) v[0] = halve(v[0], o);
+      for (int o = 8; o > 0; o >>= 1) v[0] = halve(v[0], o);
       turn ^= 1;
     }
   } else {
@@ -189,15 +194,13 @@ __device__ __forceinline__ void row_sum(float (&v)[K], SumBuffer<L, K>& buf, int
     for (int o = 4; o > 0; o >>= 1) x = halve(x, o);
     if ((lane & 7) == 0) buf.part[turn][mine][threadIdx.x >> 5] = x;
     __syncthreads();
-    x = buf.part[turn][mine][lane & (n < 8 ? n - 1 : 7)];
-    if (n > 8) x += buf.part[turn][mine][(lane & 7) + (n > 8 ? 8 : 0)];
+    x = buf.part[turn][mine][lane & 7] + buf.part[turn][mine][(lane & 7) + 8];
 #pragma unroll
-    for (int o = n < 8 ? n / 2 : 4; o > 0; o >>= 1) x = halve(x, o);
+    for (int o = 4; o > 0; o >>= 1) x = halve(x, o);
 #pragma unroll
     for (int k = 0; k < K; ++k) v[k] = __shfl_sync(0xffffffffu, x, 8 * k);
     turn ^= 1;
   }
-  static_assert(n == 4 || n == 8 || n == 16, "warps of a CTA");
 }
 
 // 1 / (1 + exp(-z)) from the approximate power and reciprocal: a few units in
@@ -235,47 +238,52 @@ __device__ __forceinline__ void gate_slope(int act, F<P> z, F<P>* a, F<P>* da) {
 // A CTA's partial sums of one weight gradient, one row of D values: its rows'
 // groups of threads are added in order through shared memory.
 template <typename L>
-__device__ __forceinline__ void store_partial(float* part, const F<L::P> (&acc)[L::N], float* smem,
-                                              const Place<L>& at) {
-  if constexpr (L::kRows == 1) {
-    store_row<L, float>(part, acc, at, true);
+__device__ __forceinline__ void store_partial(float* part, const F<L::P> (&acc)[L::NV][L::G],
+                                              float* smem, const Place<L>& at) {
+  if constexpr (!L::kShort) {
+#pragma unroll
+    for (int j = 0; j < L::NV; ++j)
+      if (at.has(j)) store_vector<L, float>(part + at.channel(j), acc[j]);
   } else {
-    constexpr int kRow = L::TPR * L::NV * L::V;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < L::N; ++i)
+    for (int j = 0; j < L::NV; ++j)
 #pragma unroll
-      for (int e = 0; e < L::P; ++e) {
-        const int k = i * L::P + e;
-        smem[at.sub * kRow + at.c0 + (k / L::V) * L::TPR * L::V + k % L::V] = acc[i].v[e];
-      }
+      for (int e = 0; e < L::V; ++e)
+        smem[at.sub * L::kMost + at.channel(j) + e] = acc[j][e / L::P].v[e % L::P];
     __syncthreads();
     for (unsigned c = threadIdx.x; c < at.D; c += L::TH) {
       float s = 0.f;
-      for (int i = 0; i < L::kRows; ++i) s += smem[i * kRow + c];
+      for (int i = 0; i < L::kRows; ++i) s += smem[i * L::kMost + c];
       part[c] = s;
     }
   }
 }
 
 // Calls f.template run<Layout>() with the layout for rows of D channels: vectors
-// of four where D is a multiple of 4 and every array starts on one (`wide`: 8
-// bytes of bf16, 16 of fp32), else single elements.
-template <typename F>
-int with_layout(int D, bool wide, F&& f) {
-  if (wide && D % 4 == 0) {
+// of four where D is a multiple of 4 and every array starts on one (`width` 4: 8
+// bytes of bf16, 16 of fp32), pairs where D is even and they start on one, else
+// single channels.  LONG: vectors of a thread in rows of 257 to 4096 channels.
+template <int LONG, typename F>
+int with_layout(int D, int width, F&& f) {
+  if (width == 4 && D % 4 == 0) {
     if (D <= 64) return f.template run<Layout<8, 256, 2, 4>>();
     if (D <= 128) return f.template run<Layout<16, 256, 2, 4>>();
     if (D <= 256) return f.template run<Layout<32, 256, 2, 4>>();
-    if (D <= 1024) return f.template run<Layout<128, 128, 2, 4>>();
-    if (D <= 2048) return f.template run<Layout<256, 256, 2, 4>>();
-    if (D <= 4096) return f.template run4096();
-    if (D <= 8192) return f.template run<Layout<512, 512, 4, 4>>();
-    return f.template run<Layout<512, 512, 8, 4>>();
+    if (D <= 4096) return f.template run<Layout<0, 1024 / LONG, LONG, 4>>();
+    if (D <= 8192) return f.template run<Layout<0, 512, 4, 4>>();
+    return f.template run<Layout<0, 512, 8, 4>>();
   }
+  if (width >= 2 && D % 2 == 0) {
+    if (D <= 32) return f.template run<Layout<8, 256, 2, 2>>();
+    if (D <= 256) return f.template run<Layout<32, 256, 4, 2>>();
+    if (D <= 4096) return f.template run<Layout<0, 512, 4, 2>>();
+    return f.template run<Layout<0, 512, 16, 2>>();
+  }
+  if (D <= 32) return f.template run<Layout<8, 256, 4, 1>>();
   if (D <= 256) return f.template run<Layout<32, 256, 8, 1>>();
-  if (D <= 2048) return f.template run<Layout<256, 256, 8, 1>>();
-  return f.template run<Layout<512, 512, 32, 1>>();
+  if (D <= 4096) return f.template run<Layout<0, 512, 8, 1>>();
+  return f.template run<Layout<0, 512, 32, 1>>();
 }
 
 // dst[i] = sum over parts p < n of part[p][i], i < cols.

@@ -16,7 +16,8 @@ namespace {
 
 template <typename L, typename TX, typename T>
 __global__ void __launch_bounds__(L::TH) gated_norm_kernel(const GatedNormArgs a) {
-  constexpr int kAll = sizeof(TX) + sizeof(T), kStages = stages(kAll), P = L::P, N = L::N;
+  constexpr int kAll = sizeof(TX) + sizeof(T), kStages = stages<L>(kAll);
+  constexpr int P = L::P, G = L::G, NV = L::NV;
   using RX = Ring<L, TX, 0, kAll>;
   using RZ = Ring<L, T, sizeof(TX), kAll>;
   extern __shared__ __align__(16) unsigned char smem[];
@@ -37,53 +38,64 @@ __global__ void __launch_bounds__(L::TH) gated_norm_kernel(const GatedNormArgs a
     next += stride;
     to = to == kStages - 1 ? 0 : to + 1;
   };
-  if constexpr (L::kStaged) {
+  if constexpr (kStages > 0) {
     RX::clear(smem, at);
     RZ::clear(smem, at);
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) fetch();
   }
-  F<P> w[N];
-  load_weight<L>(w, a.w, a.offset, at);
+  sum_init(buf);
+  F<P> w[NV][G];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) load_weight<L>(w[j], a.w, a.offset, j, at);
   const float inv = 1.f / float(a.D);
   for (; row - at.sub < a.rows; row += stride) {
     const bool on = !L::kShort || row < a.rows;
     const size_t o = size_t(on ? row : 0) * a.D;
-    F<P> x[N], z[N];
-    if constexpr (L::kStaged) {
+    const TX* px = static_cast<const TX*>(a.x) + o;
+    const T* pz = static_cast<const T*>(a.z) + o;
+    F<P> x[NV][G], z[NV][G];
+    if constexpr (kStages > 0) {
       copies_wait<kStages>();
-      RX::take(x, smem, stage);
-      if (a.z) RZ::take(z, smem, stage);
-      stage = stage == kStages - 1 ? 0 : stage + 1;
-      fetch();
-    } else {
-      load_row<L, TX>(x, static_cast<const TX*>(a.x) + o, at, on);
-      if (a.z) load_row<L, T>(z, static_cast<const T*>(a.z) + o, at, on);
+      fetch();  // over the stage before this one
     }
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      RX::take(x[j], smem, stage, px, j, at, on);
+      if (a.z) RZ::take(z[j], smem, stage, pz, j, at, on);
+    }
+    if constexpr (kStages > 0) stage = stage == kStages - 1 ? 0 : stage + 1;
     F<P> sq = all<P>(0.f);
 #pragma unroll
-    for (int i = 0; i < N; ++i) sq = fma(x[i], x[i], sq);
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int i = 0; i < G; ++i) sq = fma(x[j][i], x[j][i], sq);
     float s[1] = {total(sq)};
     row_sum<L, 1>(s, buf, turn);
     const F<P> rstd = all<P>(rsqrtf(fmaf(s[0], inv, a.eps)));
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      x[i] = mul(mul(x[i], rstd), w[i]);
-      if (a.z) x[i] = mul(x[i], gate(a.act, z[i]));
+    for (int j = 0; j < NV; ++j) {
+#pragma unroll
+      for (int i = 0; i < G; ++i) {
+        x[j][i] = mul(mul(x[j][i], rstd), w[j][i]);
+        if (a.z) x[j][i] = mul(x[j][i], gate(a.act, z[j][i]));
+      }
+      if (on && at.has(j)) store_vector<L, T>(static_cast<T*>(a.y) + o + at.channel(j), x[j]);
     }
-    store_row<L, T>(static_cast<T*>(a.y) + o, x, at, on);
   }
 }
 
 template <typename L, typename TX, typename T>
-__global__ void __launch_bounds__(L::TH) gated_norm_backward_kernel(const GatedNormArgs a) {
-  constexpr int kAll = sizeof(TX) + 2 * sizeof(T), kStages = stages(kAll), P = L::P, N = L::N;
+__global__ void __launch_bounds__(L::TH, L::TH == 512 && L::NV * L::V == 8 ? 2 : 1)
+    gated_norm_backward_kernel(const GatedNormArgs a) {
+  constexpr int kAll = sizeof(TX) + 2 * sizeof(T), kStages = stages<L>(kAll);
+  constexpr int P = L::P, G = L::G, NV = L::NV;
   using RX = Ring<L, TX, 0, kAll>;
   using RD = Ring<L, T, sizeof(TX), kAll>;
   using RZ = Ring<L, T, sizeof(TX) + sizeof(T), kAll>;
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ SumBuffer<L, 2> buf;
-  __shared__ float groups[L::kShort ? L::TH * L::NV * L::V : 1];
+  __shared__ float groups[L::kShort ? L::kRows * L::kMost : 1];
   const Place<L> at(a.D);
   const long long stride = (long long)gridDim.x * L::kRows;
   long long row = (long long)blockIdx.x * L::kRows + at.sub, next = row;
@@ -100,67 +112,77 @@ __global__ void __launch_bounds__(L::TH) gated_norm_backward_kernel(const GatedN
     next += stride;
     to = to == kStages - 1 ? 0 : to + 1;
   };
-  if constexpr (L::kStaged) {
+  if constexpr (kStages > 0) {
     RX::clear(smem, at);
     RD::clear(smem, at);
     RZ::clear(smem, at);
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) fetch();
   }
-  F<P> w[N], dw[N];
-  load_weight<L>(w, a.w, a.offset, at);
+  sum_init(buf);
+  F<P> w[NV][G], dw[NV][G];
 #pragma unroll
-  for (int i = 0; i < N; ++i) dw[i] = all<P>(0.f);
+  for (int j = 0; j < NV; ++j) {
+    load_weight<L>(w[j], a.w, a.offset, j, at);
+#pragma unroll
+    for (int i = 0; i < G; ++i) dw[j][i] = all<P>(0.f);
+  }
   const float inv = 1.f / float(a.D);
   for (; row - at.sub < a.rows; row += stride) {
     const bool on = !L::kShort || row < a.rows;
     const size_t o = size_t(on ? row : 0) * a.D;
-    F<P> x[N], dy[N], z[N];
-    if constexpr (L::kStaged) {
+    const TX* px = static_cast<const TX*>(a.x) + o;
+    const T *pd = static_cast<const T*>(a.dy) + o, *pz = static_cast<const T*>(a.z) + o;
+    F<P> x[NV][G], dy[NV][G], z[NV][G];
+    if constexpr (kStages > 0) {
       copies_wait<kStages>();
-      RX::take(x, smem, stage);
-      RD::take(dy, smem, stage);
-      if (a.z) RZ::take(z, smem, stage);
-      stage = stage == kStages - 1 ? 0 : stage + 1;
-      fetch();
-    } else {
-      load_row<L, TX>(x, static_cast<const TX*>(a.x) + o, at, on);
-      load_row<L, T>(dy, static_cast<const T*>(a.dy) + o, at, on);
-      if (a.z) load_row<L, T>(z, static_cast<const T*>(a.z) + o, at, on);
+      fetch();  // over the stage before this one
     }
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      RX::take(x[j], smem, stage, px, j, at, on);
+      RD::take(dy[j], smem, stage, pd, j, at, on);
+      if (a.z) RZ::take(z[j], smem, stage, pz, j, at, on);
+    }
+    if constexpr (kStages > 0) stage = stage == kStages - 1 ? 0 : stage + 1;
     F<P> sq = all<P>(0.f), su = all<P>(0.f);
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      sq = fma(x[i], x[i], sq);
-      if (a.z) {
-        F<P> av, da;
-        gate_slope(a.act, z[i], &av, &da);
-        z[i] = mul(mul(mul(dy[i], w[i]), x[i]), da);  // dz, but for rstd
-        dy[i] = mul(dy[i], av);                       // u without w
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int i = 0; i < G; ++i) {
+        sq = fma(x[j][i], x[j][i], sq);
+        if (a.z) {
+          F<P> av, da;
+          gate_slope(a.act, z[j][i], &av, &da);
+          z[j][i] = mul(mul(mul(dy[j][i], w[j][i]), x[j][i]), da);  // dz, but for rstd
+          dy[j][i] = mul(dy[j][i], av);                             // u without w
+        }
+        su = fma(mul(dy[j][i], w[j][i]), x[j][i], su);
       }
-      su = fma(mul(dy[i], w[i]), x[i], su);
-    }
     float s[2] = {total(sq), total(su)};
     row_sum<L, 2>(s, buf, turn);
     const float r = rsqrtf(fmaf(s[0], inv, a.eps));
     const F<P> rstd = all<P>(r), c = all<P>(-(s[1] * inv * r * r));  // -mean(u xh) rstd
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      dw[i] = fma(dy[i], mul(x[i], rstd), dw[i]);
-      x[i] = mul(rstd, fma(c, x[i], mul(dy[i], w[i])));
-    }
-    store_row<L, TX>(static_cast<TX*>(a.dx) + o, x, at, on);
-    if (a.z) {
+    for (int j = 0; j < NV; ++j) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) z[i] = mul(z[i], rstd);
-      store_row<L, T>(static_cast<T*>(a.dz) + o, z, at, on);
+      for (int i = 0; i < G; ++i) {
+        dw[j][i] = fma(dy[j][i], mul(x[j][i], rstd), dw[j][i]);
+        x[j][i] = mul(rstd, fma(c, x[j][i], mul(dy[j][i], w[j][i])));
+        if (a.z) z[j][i] = mul(z[j][i], rstd);
+      }
+      if (on && at.has(j)) {
+        store_vector<L, TX>(static_cast<TX*>(a.dx) + o + at.channel(j), x[j]);
+        if (a.z) store_vector<L, T>(static_cast<T*>(a.dz) + o + at.channel(j), z[j]);
+      }
     }
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   store_partial<L>(a.part + size_t(blockIdx.x) * a.D, dw, groups, at);
 }
 
-constexpr long long kForwardCtas = 16;  // per SM: 8 rows of a CTA at a time are resident
+// Threads of all CTAs per SM; more than are resident where CTAs end early.
+constexpr int kForwardThreads = 2048, kBackwardThreads = 1024;
 
 template <typename TX, typename T>
 struct Forward {
@@ -169,14 +191,15 @@ struct Forward {
   cudaStream_t stream;
   template <typename L>
   int run() {
+    const int threads = norm_threads<L>(a.D);
     const long long groups = (a.rows + L::kRows - 1) / L::kRows;
-    const int grid = int(std::min(groups, kForwardCtas * sms));
-    constexpr size_t smem = ring_bytes<L>(sizeof(TX) + sizeof(T));
-    if (!raise_smem<&gated_norm_kernel<L, TX, T>>(smem)) return GDN_ERR_LAUNCH;
-    gated_norm_kernel<L, TX, T><<<grid, L::TH, smem, stream>>>(a);
+    const int grid = int(std::min<long long>(groups, kForwardThreads / threads * (long long)sms));
+    constexpr int kBytes = sizeof(TX) + sizeof(T);
+    constexpr size_t kThread = stages<L>(kBytes) * L::NV * L::V * kBytes;
+    if (!raise_smem<&gated_norm_kernel<L, TX, T>>(kThread * L::TH)) return GDN_ERR_LAUNCH;
+    gated_norm_kernel<L, TX, T><<<grid, threads, kThread * threads, stream>>>(a);
     return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_LAUNCH;
   }
-  int run4096() { return run<Layout<256, 256, 4, 4>>(); }
 };
 
 template <typename TX, typename T>
@@ -186,45 +209,52 @@ struct Backward {
   cudaStream_t stream;
   template <typename L>
   int run() {
+    const int threads = norm_threads<L>(a.D);
     const long long groups = (a.rows + L::kRows - 1) / L::kRows;
-    const int grid = int(std::min<long long>(groups, norm_max_parts(a.rows, a.D)));
-    constexpr size_t smem = ring_bytes<L>(sizeof(TX) + 2 * sizeof(T));
-    if (!raise_smem<&gated_norm_backward_kernel<L, TX, T>>(smem)) return GDN_ERR_LAUNCH;
-    gated_norm_backward_kernel<L, TX, T><<<grid, L::TH, smem, stream>>>(a);
+    const int per_sm = std::max(1, (L::kShort ? 512 : kBackwardThreads) / threads);
+    const int grid = int(std::min({groups, (long long)norm_max_parts(a.rows, a.D),
+                                   (long long)per_sm * sms}));
+    constexpr int kBytes = sizeof(TX) + 2 * sizeof(T);
+    constexpr size_t kThread = stages<L>(kBytes) * L::NV * L::V * kBytes;
+    if (!raise_smem<&gated_norm_backward_kernel<L, TX, T>>(kThread * L::TH)) return GDN_ERR_LAUNCH;
+    gated_norm_backward_kernel<L, TX, T><<<grid, threads, kThread * threads, stream>>>(a);
     if (cudaGetLastError() != cudaSuccess) return GDN_ERR_LAUNCH;
     return launch_reduce_parts(a.part, grid, a.D, &a.dw, a.D, stream);
   }
-  int run4096() { return run<Layout<512, 512, 2, 4>>(); }
 };
 
-// Whether every array starts on four elements.
-bool wide_ok(const GatedNormArgs& a, int x_dtype, int dtype) {
-  const uintptr_t ex = x_dtype == GDN_BF16 ? 8 : 16, e = dtype == GDN_BF16 ? 8 : 16;
-  return aligned(a.x, ex) && aligned(a.dx, ex) && aligned(a.z, e) && aligned(a.y, e) &&
-         aligned(a.dy, e) && aligned(a.dz, e) && aligned(a.w, 16);
+// How many elements every array starts on a multiple of: 4, 2 or 1.
+int width(const GatedNormArgs& a, int x_dtype, int dtype) {
+  const uintptr_t ex = x_dtype == GDN_BF16 ? 2 : 4, e = dtype == GDN_BF16 ? 2 : 4;
+  const auto ok = [&](uintptr_t n) {
+    return aligned(a.x, n * ex) && aligned(a.dx, n * ex) && aligned(a.z, n * e) &&
+           aligned(a.y, n * e) && aligned(a.dy, n * e) && aligned(a.dz, n * e) &&
+           aligned(a.w, n * 4);
+  };
+  return ok(4) ? 4 : ok(2) ? 2 : 1;
 }
 
-template <template <typename, typename> class Run>
+template <template <typename, typename> class Run, int LONG>
 int dispatch(const GatedNormArgs& a, int x_dtype, int dtype, int sms, cudaStream_t stream) {
   using B = __nv_bfloat16;
-  const bool wide = wide_ok(a, x_dtype, dtype);
+  const int n = width(a, x_dtype, dtype);
   if (x_dtype == GDN_BF16)
-    return dtype == GDN_BF16 ? with_layout(a.D, wide, Run<B, B>{a, sms, stream})
-                             : with_layout(a.D, wide, Run<B, float>{a, sms, stream});
-  return dtype == GDN_BF16 ? with_layout(a.D, wide, Run<float, B>{a, sms, stream})
-                           : with_layout(a.D, wide, Run<float, float>{a, sms, stream});
+    return dtype == GDN_BF16 ? with_layout<LONG>(a.D, n, Run<B, B>{a, sms, stream})
+                             : with_layout<LONG>(a.D, n, Run<B, float>{a, sms, stream});
+  return dtype == GDN_BF16 ? with_layout<LONG>(a.D, n, Run<float, B>{a, sms, stream})
+                           : with_layout<LONG>(a.D, n, Run<float, float>{a, sms, stream});
 }
 
 }  // namespace
 
 int launch_gated_norm(const GatedNormArgs& a, int x_dtype, int dtype, int sms,
                       cudaStream_t stream) {
-  return dispatch<Forward>(a, x_dtype, dtype, sms, stream);
+  return dispatch<Forward, 4>(a, x_dtype, dtype, sms, stream);
 }
 
 int launch_gated_norm_backward(const GatedNormArgs& a, int x_dtype, int dtype, int sms,
                                cudaStream_t stream) {
-  return dispatch<Backward>(a, x_dtype, dtype, sms, stream);
+  return dispatch<Backward, 2>(a, x_dtype, dtype, sms, stream);
 }
 
 }  // namespace gdn

@@ -19,7 +19,8 @@ namespace {
 
 template <typename L, typename T, typename TR>
 __global__ void __launch_bounds__(L::TH) residual_norm_kernel(const ResidualNormArgs a) {
-  constexpr int kAll = 2 * sizeof(T) + sizeof(TR), kStages = stages(kAll), P = L::P, N = L::N;
+  constexpr int kAll = 2 * sizeof(T) + sizeof(TR), kStages = stages<L>(kAll);
+  constexpr int P = L::P, G = L::G, NV = L::NV;
   using RR = Ring<L, TR, 0, kAll>;
   using RX = Ring<L, T, sizeof(TR), kAll>;
   using RZ = Ring<L, T, sizeof(TR) + sizeof(T), kAll>;
@@ -42,67 +43,85 @@ __global__ void __launch_bounds__(L::TH) residual_norm_kernel(const ResidualNorm
     next += stride;
     to = to == kStages - 1 ? 0 : to + 1;
   };
-  if constexpr (L::kStaged) {
+  if constexpr (kStages > 0) {
     RR::clear(smem, at);
     RX::clear(smem, at);
     RZ::clear(smem, at);
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) fetch();
   }
-  F<P> w[N], wp[N];  // wp: the post norm's weight times the scale
-  load_weight<L>(w, a.scale, 0.f, at);
-  load_weight<L>(wp, a.w_post, a.offset, at);
+  sum_init(buf);
+  F<P> w[NV][G], wp[NV][G];  // wp: the post norm's weight times the scale
 #pragma unroll
-  for (int i = 0; i < N; ++i) wp[i] = mul(wp[i], w[i]);
-  load_weight<L>(w, a.w, a.offset, at);
+  for (int j = 0; j < NV; ++j) {
+    load_weight<L>(w[j], a.scale, 0.f, j, at);
+    load_weight<L>(wp[j], a.w_post, a.offset, j, at);
+#pragma unroll
+    for (int i = 0; i < G; ++i) wp[j][i] = mul(wp[j][i], w[j][i]);
+    load_weight<L>(w[j], a.w, a.offset, j, at);
+  }
   const float inv = 1.f / float(a.D);
   for (; row - at.sub < a.rows; row += stride) {
     const bool on = !L::kShort || row < a.rows;
     const size_t o = size_t(on ? row : 0) * a.D;
-    F<P> x[N], r[N], z[N];
-    if constexpr (L::kStaged) {
+    const T *px = static_cast<const T*>(a.x) + o, *pz = static_cast<const T*>(a.z) + o;
+    const TR* pr = static_cast<const TR*>(a.r) + o;
+    F<P> x[NV][G], r[NV][G], z[NV][G];
+    if constexpr (kStages > 0) {
       copies_wait<kStages>();
-      RX::take(x, smem, stage);
-      RR::take(r, smem, stage);
-      if (a.z) RZ::take(z, smem, stage);
-      stage = stage == kStages - 1 ? 0 : stage + 1;
-      fetch();
-    } else {
-      load_row<L, T>(x, static_cast<const T*>(a.x) + o, at, on);
-      load_row<L, TR>(r, static_cast<const TR*>(a.r) + o, at, on);
-      if (a.z) load_row<L, T>(z, static_cast<const T*>(a.z) + o, at, on);
+      fetch();  // over the stage before this one
     }
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      RX::take(x[j], smem, stage, px, j, at, on);
+      RR::take(r[j], smem, stage, pr, j, at, on);
+      if (a.z) RZ::take(z[j], smem, stage, pz, j, at, on);
+    }
+    if constexpr (kStages > 0) stage = stage == kStages - 1 ? 0 : stage + 1;
     float rstd = 1.f;
     if (a.w_post) {
       F<P> sq = all<P>(0.f);
 #pragma unroll
-      for (int i = 0; i < N; ++i) sq = fma(x[i], x[i], sq);
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int i = 0; i < G; ++i) sq = fma(x[j][i], x[j][i], sq);
       float s[1] = {total(sq)};
       row_sum<L, 1>(s, buf, turn);
       rstd = rsqrtf(fmaf(s[0], inv, a.eps));
     }
     F<P> sq = all<P>(0.f);
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      x[i] = mul(x[i], all<P>(rstd));
-      if (a.z) x[i] = mul(x[i], gate(a.act, z[i]));
-      r[i] = fma(x[i], wp[i], r[i]);
-      sq = fma(r[i], r[i], sq);
+    for (int j = 0; j < NV; ++j) {
+#pragma unroll
+      for (int i = 0; i < G; ++i) {
+        x[j][i] = mul(x[j][i], all<P>(rstd));
+        if (a.z) x[j][i] = mul(x[j][i], gate(a.act, z[j][i]));
+        r[j][i] = fma(x[j][i], wp[j][i], r[j][i]);
+        sq = fma(r[j][i], r[j][i], sq);
+      }
+      if (on && at.has(j)) store_vector<L, TR>(static_cast<TR*>(a.r_out) + o + at.channel(j), r[j]);
     }
-    store_row<L, TR>(static_cast<TR*>(a.r_out) + o, r, at, on);
     float s[1] = {total(sq)};
     row_sum<L, 1>(s, buf, turn);
     const F<P> rs = all<P>(rsqrtf(fmaf(s[0], inv, a.eps)));
 #pragma unroll
-    for (int i = 0; i < N; ++i) r[i] = mul(mul(r[i], rs), w[i]);
-    store_row<L, T>(static_cast<T*>(a.y) + o, r, at, on);
+    for (int j = 0; j < NV; ++j) {
+#pragma unroll
+      for (int i = 0; i < G; ++i) r[j][i] = mul(mul(r[j][i], rs), w[j][i]);
+      if (on && at.has(j)) store_vector<L, T>(static_cast<T*>(a.y) + o + at.channel(j), r[j]);
+    }
   }
 }
 
+// A thread with more than 8 channels has no registers for its inputs and weights
+// beside the sums: it takes each vector again from the ring (or from memory) and
+// the weights from the cache for every pass over the row.
 template <typename L, typename T, typename TR>
 __global__ void __launch_bounds__(L::TH) residual_norm_backward_kernel(const ResidualNormArgs a) {
-  constexpr int kT = sizeof(T), kR = sizeof(TR), kAll = 3 * kT + 2 * kR, kStages = stages(kAll);
-  constexpr int P = L::P, N = L::N;
+  constexpr int kT = sizeof(T), kR = sizeof(TR), kAll = 3 * kT + 2 * kR, kStages = stages<L>(kAll);
+  constexpr int P = L::P, G = L::G, NV = L::NV;
+  constexpr bool kKeep = NV * L::V <= 8;
+  constexpr int KV = kKeep ? NV : 1;  // vectors kept
   using RR = Ring<L, TR, 0, kAll>;
   using RG = Ring<L, TR, kR, kAll>;
   using RD = Ring<L, T, 2 * kR, kAll>;
@@ -111,7 +130,7 @@ __global__ void __launch_bounds__(L::TH) residual_norm_backward_kernel(const Res
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ SumBuffer<L, 3> buf3;
   __shared__ SumBuffer<L, 1> buf1;
-  __shared__ float groups[L::kShort ? L::TH * L::NV * L::V : 1];
+  __shared__ float groups[L::kShort ? L::kRows * L::kMost : 1];
   const Place<L> at(a.D);
   const long long stride = (long long)gridDim.x * L::kRows;
   long long row = (long long)blockIdx.x * L::kRows + at.sub, next = row;
@@ -130,7 +149,7 @@ __global__ void __launch_bounds__(L::TH) residual_norm_backward_kernel(const Res
     next += stride;
     to = to == kStages - 1 ? 0 : to + 1;
   };
-  if constexpr (L::kStaged) {
+  if constexpr (kStages > 0) {
     RR::clear(smem, at);
     RG::clear(smem, at);
     RD::clear(smem, at);
@@ -139,43 +158,70 @@ __global__ void __launch_bounds__(L::TH) residual_norm_backward_kernel(const Res
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) fetch();
   }
-  F<P> w[N], wp[N], sc[N], dw[N], dwp[N], dsc[N];
-  load_weight<L>(w, a.w, a.offset, at);
-  load_weight<L>(wp, a.w_post, a.offset, at);
-  load_weight<L>(sc, a.scale, 0.f, at);
+  sum_init(buf3);
+  sum_init(buf1);
+  F<P> w[KV][G], wp[KV][G], sc[KV][G], dw[NV][G], dwp[NV][G], dsc[NV][G];
+  const auto weights = [&](int j) {
+    F<P>(&wj)[G] = w[kKeep ? j : 0];
+    load_weight<L>(wj, a.w, a.offset, j, at);
+    load_weight<L>(wp[kKeep ? j : 0], a.w_post, a.offset, j, at);
+    load_weight<L>(sc[kKeep ? j : 0], a.scale, 0.f, j, at);
+  };
 #pragma unroll
-  for (int i = 0; i < N; ++i) dw[i] = dwp[i] = dsc[i] = all<P>(0.f);
+  for (int j = 0; j < NV; ++j) {
+    if (kKeep) weights(j);
+#pragma unroll
+    for (int i = 0; i < G; ++i) dw[j][i] = dwp[j][i] = dsc[j][i] = all<P>(0.f);
+  }
   const float inv = 1.f / float(a.D);
   for (; row - at.sub < a.rows; row += stride) {
     const bool on = !L::kShort || row < a.rows;
     const size_t o = size_t(on ? row : 0) * a.D;
-    F<P> x[N], z[N], dy[N], r[N], q[N];
-    if constexpr (L::kStaged) {
+    const T *px = static_cast<const T*>(a.x) + o, *pz = static_cast<const T*>(a.z) + o,
+            *pd = static_cast<const T*>(a.dy) + o;
+    const TR *pr = static_cast<const TR*>(a.r) + o, *pg = static_cast<const TR*>(a.dr_out) + o;
+    F<P> x[KV][G], z[KV][G], dy[KV][G], r[KV][G], q[KV][G], v[NV][G];
+    if constexpr (kStages > 0) {
       copies_wait<kStages>();
-      RR::take(r, smem, stage);
-      RD::take(dy, smem, stage);
-      RX::take(x, smem, stage);
-      if (a.dr_out) RG::take(q, smem, stage);
-      if (a.z) RZ::take(z, smem, stage);
-      stage = stage == kStages - 1 ? 0 : stage + 1;
-      fetch();
-    } else {
-      load_row<L, TR>(r, static_cast<const TR*>(a.r) + o, at, on);
-      load_row<L, T>(dy, static_cast<const T*>(a.dy) + o, at, on);
-      load_row<L, T>(x, static_cast<const T*>(a.x) + o, at, on);
-      if (a.dr_out) load_row<L, TR>(q, static_cast<const TR*>(a.dr_out) + o, at, on);
-      if (a.z) load_row<L, T>(z, static_cast<const T*>(a.z) + o, at, on);
+      fetch();  // over the stage before this one
     }
-    if (!a.dr_out) {
+    const int here = stage;
+    // the vectors of the first sum, and those of the second besides
+    const auto take = [&](int j, bool rest) {
+      const int k = kKeep ? j : 0;
+      if (!kKeep || !rest) {
+        RR::take(r[k], smem, here, pr, j, at, on);
+        RD::take(dy[k], smem, here, pd, j, at, on);
+        RX::take(x[k], smem, here, px, j, at, on);
+      }
+      if (kKeep != rest) {
+        if (a.dr_out) {
+          RG::take(q[k], smem, here, pg, j, at, on);
+        } else {
 #pragma unroll
-      for (int i = 0; i < N; ++i) q[i] = all<P>(0.f);
-    }
+          for (int i = 0; i < G; ++i) q[k][i] = all<P>(0.f);
+        }
+        if (a.z) RZ::take(z[k], smem, here, pz, j, at, on);
+      }
+    };
     F<P> s0 = all<P>(0.f), s1 = s0, s2 = s0;
+    if (kKeep) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      s0 = fma(r[i], r[i], s0);
-      s1 = fma(mul(dy[i], w[i]), r[i], s1);
-      s2 = fma(x[i], x[i], s2);
+      for (int j = 0; j < NV; ++j) take(j, false);
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int k = kKeep ? j : 0;
+      if (!kKeep) {
+        take(j, false);
+        load_weight<L>(w[k], a.w, a.offset, j, at);
+      }
+#pragma unroll
+      for (int i = 0; i < G; ++i) {
+        s0 = fma(r[k][i], r[k][i], s0);
+        s1 = fma(mul(dy[k][i], w[k][i]), r[k][i], s1);
+        s2 = fma(x[k][i], x[k][i], s2);
+      }
     }
     float s[3] = {total(s0), total(s1), total(s2)};
     row_sum<L, 3>(s, buf3, turn3);
@@ -184,33 +230,57 @@ __global__ void __launch_bounds__(L::TH) residual_norm_backward_kernel(const Res
     const F<P> rr = all<P>(rs), c = all<P>(-(s[1] * inv * rs * rs)), rp = all<P>(rx);
     F<P> sm = all<P>(0.f);
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      q[i] = fma(rr, fma(c, r[i], mul(dy[i], w[i])), q[i]);
-      dw[i] = fma(dy[i], mul(r[i], rr), dw[i]);
-      x[i] = mul(x[i], rp);  // xh
-      const F<P> u = mul(x[i], wp[i]);
-      F<P> qa = q[i];
-      if (a.z) {
-        F<P> av, da;
-        gate_slope(a.act, z[i], &av, &da);
-        qa = mul(qa, av);
-        z[i] = mul(mul(mul(q[i], sc[i]), u), da);  // dz
+    for (int j = 0; j < NV; ++j) {
+      const int k = kKeep ? j : 0;
+      if (!kKeep) {
+        take(j, true);
+        weights(j);
       }
-      dsc[i] = fma(qa, u, dsc[i]);
-      r[i] = mul(qa, sc[i]);  // v
-      dwp[i] = fma(r[i], x[i], dwp[i]);
-      sm = fma(r[i], u, sm);
+#pragma unroll
+      for (int i = 0; i < G; ++i) {
+        q[k][i] = fma(rr, fma(c, r[k][i], mul(dy[k][i], w[k][i])), q[k][i]);
+        dw[j][i] = fma(dy[k][i], mul(r[k][i], rr), dw[j][i]);
+        x[k][i] = mul(x[k][i], rp);  // xh
+        const F<P> u = mul(x[k][i], wp[k][i]);
+        F<P> qa = q[k][i];
+        if (a.z) {
+          F<P> av, da;
+          gate_slope(a.act, z[k][i], &av, &da);
+          qa = mul(qa, av);
+          z[k][i] = mul(mul(mul(q[k][i], sc[k][i]), u), da);  // dz
+        }
+        dsc[j][i] = fma(qa, u, dsc[j][i]);
+        v[j][i] = mul(qa, sc[k][i]);
+        dwp[j][i] = fma(v[j][i], x[k][i], dwp[j][i]);
+        sm = fma(v[j][i], u, sm);
+      }
+      if (on && at.has(j)) {
+        store_vector<L, TR>(static_cast<TR*>(a.dr) + o + at.channel(j), q[k]);
+        if (a.z) store_vector<L, T>(static_cast<T*>(a.dz) + o + at.channel(j), z[k]);
+      }
     }
-    store_row<L, TR>(static_cast<TR*>(a.dr) + o, q, at, on);
-    if (a.z) store_row<L, T>(static_cast<T*>(a.dz) + o, z, at, on);
     if (a.w_post) {
       float m[1] = {total(sm)};
       row_sum<L, 1>(m, buf1, turn1);
-      const F<P> k = all<P>(-(m[0] * inv));  // -mean(v w_post xh)
+      const F<P> e = all<P>(-(m[0] * inv));  // -mean(v w_post xh)
 #pragma unroll
-      for (int i = 0; i < N; ++i) r[i] = mul(rp, fma(k, x[i], mul(r[i], wp[i])));
+      for (int j = 0; j < NV; ++j) {
+        const int k = kKeep ? j : 0;
+        if (!kKeep) {
+          RX::take(x[k], smem, here, px, j, at, on);
+          load_weight<L>(wp[k], a.w_post, a.offset, j, at);
+#pragma unroll
+          for (int i = 0; i < G; ++i) x[k][i] = mul(x[k][i], rp);
+        }
+#pragma unroll
+        for (int i = 0; i < G; ++i)
+          v[j][i] = mul(rp, fma(e, x[k][i], mul(v[j][i], wp[k][i])));
+      }
     }
-    store_row<L, T>(static_cast<T*>(a.dx) + o, r, at, on);
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+      if (on && at.has(j)) store_vector<L, T>(static_cast<T*>(a.dx) + o + at.channel(j), v[j]);
+    if constexpr (kStages > 0) stage = stage == kStages - 1 ? 0 : stage + 1;
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // partial gradients of the weights that there are: w, then w_post, then scale
@@ -244,7 +314,8 @@ __global__ void __launch_bounds__(32 * kReduceWarps)
   if (lane == 0 && col < cols) (col < D ? d0 : col < 2 * D ? d1 : d2)[col % D] = s;
 }
 
-constexpr long long kForwardCtas = 4;  // per SM
+// Threads of all CTAs per SM.
+constexpr int kForwardThreads = 1024, kBackwardThreads = 512;
 
 template <typename T, typename TR>
 struct Forward {
@@ -253,14 +324,15 @@ struct Forward {
   cudaStream_t stream;
   template <typename L>
   int run() {
+    const int threads = norm_threads<L>(a.D);
     const long long groups = (a.rows + L::kRows - 1) / L::kRows;
-    const int grid = int(std::min(groups, kForwardCtas * sms));
-    constexpr size_t smem = ring_bytes<L>(2 * sizeof(T) + sizeof(TR));
-    if (!raise_smem<&residual_norm_kernel<L, T, TR>>(smem)) return GDN_ERR_LAUNCH;
-    residual_norm_kernel<L, T, TR><<<grid, L::TH, smem, stream>>>(a);
+    const int grid = int(std::min<long long>(groups, kForwardThreads / threads * (long long)sms));
+    constexpr int kBytes = 2 * sizeof(T) + sizeof(TR);
+    constexpr size_t kThread = stages<L>(kBytes) * L::NV * L::V * kBytes;
+    if (!raise_smem<&residual_norm_kernel<L, T, TR>>(kThread * L::TH)) return GDN_ERR_LAUNCH;
+    residual_norm_kernel<L, T, TR><<<grid, threads, kThread * threads, stream>>>(a);
     return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_LAUNCH;
   }
-  int run4096() { return run<Layout<256, 256, 4, 4>>(); }
 };
 
 template <typename T, typename TR>
@@ -270,34 +342,42 @@ struct Backward {
   cudaStream_t stream;
   template <typename L>
   int run() {
+    const int threads = norm_threads<L>(a.D);
     const long long groups = (a.rows + L::kRows - 1) / L::kRows;
-    const int grid = int(std::min<long long>(groups, norm_max_parts(a.rows, a.D)));
-    constexpr size_t smem = ring_bytes<L>(3 * sizeof(T) + 2 * sizeof(TR));
-    if (!raise_smem<&residual_norm_backward_kernel<L, T, TR>>(smem)) return GDN_ERR_LAUNCH;
-    residual_norm_backward_kernel<L, T, TR><<<grid, L::TH, smem, stream>>>(a);
+    const int per_sm = std::max(1, kBackwardThreads / threads);
+    const int grid = int(std::min({groups, (long long)norm_max_parts(a.rows, a.D),
+                                   (long long)per_sm * sms}));
+    constexpr int kBytes = 3 * sizeof(T) + 2 * sizeof(TR);
+    constexpr size_t kThread = stages<L>(kBytes) * L::NV * L::V * kBytes;
+    if (!raise_smem<&residual_norm_backward_kernel<L, T, TR>>(kThread * L::TH))
+      return GDN_ERR_LAUNCH;
+    residual_norm_backward_kernel<L, T, TR><<<grid, threads, kThread * threads, stream>>>(a);
     if (cudaGetLastError() != cudaSuccess) return GDN_ERR_LAUNCH;
     float* dst[3] = {a.dw, a.w_post ? a.dw_post : a.dscale, a.dscale};
     return launch_reduce_parts(a.part, grid, a.D * a.weights, dst, a.D, stream);
   }
-  int run4096() { return run<Layout<512, 512, 2, 4>>(); }
 };
 
-// Whether every array starts on four elements.
-bool wide_ok(const ResidualNormArgs& a, int dtype, int r_dtype) {
-  const uintptr_t e = dtype == GDN_BF16 ? 8 : 16, er = r_dtype == GDN_BF16 ? 8 : 16;
-  return aligned(a.x, e) && aligned(a.z, e) && aligned(a.y, e) && aligned(a.dy, e) &&
-         aligned(a.dx, e) && aligned(a.dz, e) && aligned(a.r, er) && aligned(a.r_out, er) &&
-         aligned(a.dr_out, er) && aligned(a.dr, er) && aligned(a.w, 16) && aligned(a.w_post, 16) &&
-         aligned(a.scale, 16);
+// How many elements every array starts on a multiple of: 4, 2 or 1.
+int width(const ResidualNormArgs& a, int dtype, int r_dtype) {
+  const uintptr_t e = dtype == GDN_BF16 ? 2 : 4, er = r_dtype == GDN_BF16 ? 2 : 4;
+  const auto ok = [&](uintptr_t n) {
+    return aligned(a.x, n * e) && aligned(a.z, n * e) && aligned(a.y, n * e) &&
+           aligned(a.dy, n * e) && aligned(a.dx, n * e) && aligned(a.dz, n * e) &&
+           aligned(a.r, n * er) && aligned(a.r_out, n * er) && aligned(a.dr_out, n * er) &&
+           aligned(a.dr, n * er) && aligned(a.w, n * 4) && aligned(a.w_post, n * 4) &&
+           aligned(a.scale, n * 4);
+  };
+  return ok(4) ? 4 : ok(2) ? 2 : 1;
 }
 
-template <template <typename, typename> class Run>
+template <template <typename, typename> class Run, int LONG>
 int dispatch(const ResidualNormArgs& a, int dtype, int r_dtype, int sms, cudaStream_t stream) {
   using B = __nv_bfloat16;
-  const bool wide = wide_ok(a, dtype, r_dtype);
-  if (dtype == GDN_F32) return with_layout(a.D, wide, Run<float, float>{a, sms, stream});
-  return r_dtype == GDN_BF16 ? with_layout(a.D, wide, Run<B, B>{a, sms, stream})
-                             : with_layout(a.D, wide, Run<B, float>{a, sms, stream});
+  const int n = width(a, dtype, r_dtype);
+  if (dtype == GDN_F32) return with_layout<LONG>(a.D, n, Run<float, float>{a, sms, stream});
+  return r_dtype == GDN_BF16 ? with_layout<LONG>(a.D, n, Run<B, B>{a, sms, stream})
+                             : with_layout<LONG>(a.D, n, Run<B, float>{a, sms, stream});
 }
 
 }  // namespace
@@ -323,12 +403,12 @@ int launch_reduce_parts(const float* part, int n, int cols, float* const* dst, i
 
 int launch_residual_norm(const ResidualNormArgs& a, int dtype, int r_dtype, int sms,
                          cudaStream_t stream) {
-  return dispatch<Forward>(a, dtype, r_dtype, sms, stream);
+  return dispatch<Forward, 4>(a, dtype, r_dtype, sms, stream);
 }
 
 int launch_residual_norm_backward(const ResidualNormArgs& a, int dtype, int r_dtype, int sms,
                                   cudaStream_t stream) {
-  return dispatch<Backward>(a, dtype, r_dtype, sms, stream);
+  return dispatch<Backward, 2>(a, dtype, r_dtype, sms, stream);
 }
 
 }  // namespace gdn

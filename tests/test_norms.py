@@ -149,8 +149,8 @@ def test_no_rows_is_a_noop(norms):
 
 def test_workspace_bytes(norms):
     assert norms.workspace_bytes(8, 128, 1) == 8 * 128 * 4
-    assert norms.workspace_bytes(1 << 20, 128, 1) == 296 * 128 * 4
-    assert norms.workspace_bytes(1 << 20, 4096, 3) == 148 * 4096 * 12
+    assert norms.workspace_bytes(1 << 20, 128, 1) == 592 * 128 * 4
+    assert norms.workspace_bytes(1 << 20, 4096, 3) == 296 * 4096 * 12
     assert norms.workspace_bytes(0, 128) == norms.workspace_bytes(5, 0) == 0
     assert norms.workspace_bytes(5, 128, 4) == norms.workspace_bytes(-1, 128) == 0
 
