@@ -1,10 +1,11 @@
 // What the norm kernels share: the layout of a row over threads, its sums, the
 // gate, and the copies of the next rows.
 //
-// A row of D channels is held by TPR threads, NV vectors of V channels each
-// (vector j of thread t: channels (j TPR + t) V ..), so it is read from memory
-// once, whatever is summed over it.  Short rows (TPR 8, 16, 32) share a CTA and
-// sum by shuffles; longer ones have a CTA of as many warps as they need (TPR 0).
+// A row of D channels is held by a group of threads, NV vectors of V channels
+// each, so it is read from memory once, whatever is summed over it.  Short rows
+// share a CTA, TPR = 8, 16 or 32 threads a row (vector j of thread t: channels
+// (j TPR + t) V ..), and sum by shuffles; longer ones have a CTA of as many warps
+// as they need (TPR 0), each with 32 NV V neighbouring channels.
 //
 // CTAs are persistent, and each thread copies its part of the next rows to shared
 // memory asynchronously (a ring of two or three stages) while it works on the
@@ -24,42 +25,62 @@
 namespace gdn {
 
 // TH: threads of a CTA, the most of them where TPR is 0.
-template <int TPR_, int TH_, int NV_, int V_>
+template <int TPR_, int TH_, int NV_, int V_, bool ODD = false>
 struct Layout {
   static constexpr int TPR = TPR_, TH = TH_, NV = NV_, V = V_;
   static constexpr bool kShort = TPR > 0;               // several rows a CTA
+  static constexpr bool kOdd = ODD;                     // rows of an odd number of channels
   static constexpr int kRows = kShort ? TH / (TPR > 0 ? TPR : 1) : 1;
   static constexpr int P = V >= 2 ? 2 : 1;              // channels worked on together
-  static constexpr int G = V / P, N = NV * G;           // such groups of a vector, a thread
+  static constexpr int G = V / P;                       // such groups of a vector
+  static constexpr int kStep = (kShort ? TPR : 32) * V; // channels from vector to vector
   static constexpr int kMost = (kShort ? TPR : TH) * NV * V;  // channels
 };
 
 // Stages of a ring whose arrays have `bytes` a channel in all: three, or two, or
-// none where the longest row leaves no room (or copies, of 4 bytes at least and
-// slow below 8, are no help).
+// none where the longest row leaves no room (or for single channels, which may
+// have 2 bytes: copies have 4 at least).
 template <typename L>
 constexpr int stages(size_t bytes) {
   const size_t fit = 220 * 1024 / (bytes * L::TH * L::NV * L::V);
-  return L::V != 4 || fit < 2 ? 0 : fit < 3 ? 2 : 3;
+  return L::V == 1 || fit < 2 ? 0 : fit < 3 ? 2 : 3;
 }
 // Threads of a CTA for rows of D channels.
 template <typename L>
 int norm_threads(int D) {
-  return L::kShort ? L::TH : (D + L::NV * L::V * 32 - 1) / (L::NV * L::V * 32) * 32;
+  const int most = D + (L::kOdd ? 1 : 0);  // with the shift of an odd row
+  return L::kShort ? L::TH : (most + L::NV * L::V * 32 - 1) / (L::NV * L::V * 32) * 32;
 }
 
 // This thread's place: its row among the CTA's, the first channel of its vectors.
+// Of rows with an odd number of channels every second starts in the middle of an
+// aligned pair: there the pairs are shifted, -1 and 0 being the first.  A thread
+// stays with rows of one kind (CTAs step by an even number of rows).
 template <typename L>
 struct Place {
-  int sub;
-  unsigned c0, step, D;
+  int sub, c0, D;
   __device__ __forceinline__ explicit Place(int d)
       : sub(L::kShort ? threadIdx.x / (L::kShort ? L::TPR : 1) : 0),
-        c0((L::kShort ? threadIdx.x % (L::kShort ? L::TPR : 1) : threadIdx.x) * L::V),
-        step((L::kShort ? L::TPR : blockDim.x) * L::V), D(d) {}
-  __device__ __forceinline__ unsigned channel(int j) const { return c0 + j * step; }
+        c0(L::kShort ? threadIdx.x % (L::kShort ? L::TPR : 1) * L::V
+                     : (threadIdx.x >> 5) * (L::NV * L::kStep) + (threadIdx.x & 31) * L::V),
+        D(d) {
+    if (L::kOdd) c0 -= (blockIdx.x * L::kRows + sub) & 1;
+  }
+  __device__ __forceinline__ int channel(int j) const { return c0 + j * L::kStep; }
   __device__ __forceinline__ bool has(int j) const { return channel(j) < D; }
+  // channel e of vector j is one of the row's; all of them are
+  __device__ __forceinline__ bool in(int j, int e) const {
+    return !L::kOdd ? has(j) : channel(j) + e < D && (e > 0 || channel(j) >= 0);
+  }
+  __device__ __forceinline__ bool whole(int j) const {
+    return in(j, 0) && in(j, L::V - 1);
+  }
 };
+// Rows that the CTAs of a launch step by are even in number.
+template <typename L>
+int even_grid(long long grid) {
+  return int(L::kOdd && L::kRows == 1 && grid > 1 ? grid & ~1LL : grid);
+}
 
 // The channels of a vector, in groups.
 template <typename L, typename T>
@@ -67,12 +88,33 @@ __device__ __forceinline__ void spread(F<L::P> (&r)[L::G], const Vec<T, L::V>& x
 #pragma unroll
   for (int e = 0; e < L::V; ++e) r[e / L::P].v[e % L::P] = to_f(x.v[e]);
 }
+// Vector j of a row at p, channels that are not the row's as zeros.
 template <typename L, typename T>
-__device__ __forceinline__ void store_vector(T* p, const F<L::P> (&r)[L::G]) {
+__device__ __forceinline__ void load_vector(F<L::P> (&r)[L::G], const T* p, int j,
+                                            const Place<L>& at) {
+  Vec<T, L::V> x{};
+  if (!L::kOdd) {
+    if (at.has(j)) x = load<T, L::V>(p + at.channel(j));
+  } else {
+#pragma unroll
+    for (int e = 0; e < L::V; ++e)
+      if (at.in(j, e)) x.v[e] = p[at.channel(j) + e];
+  }
+  spread<L, T>(r, x);
+}
+template <typename L, typename T>
+__device__ __forceinline__ void store_vector(T* p, const F<L::P> (&r)[L::G], int j,
+                                             const Place<L>& at) {
   float x[L::V];
 #pragma unroll
   for (int e = 0; e < L::V; ++e) x[e] = r[e / L::P].v[e % L::P];
-  store<T, L::V>(p, x);
+  if (at.whole(j)) {
+    store<T, L::V>(p + at.channel(j), x);
+  } else if (L::kOdd) {
+#pragma unroll
+    for (int e = 0; e < L::V; ++e)
+      if (at.in(j, e)) p[at.channel(j) + e] = from_f<T>(x[e]);
+  }
 }
 
 // One input array in the ring: BEFORE bytes a channel of other arrays lie before
@@ -83,8 +125,9 @@ struct Ring {
   static constexpr int kStages = stages<L>(ALL);
   __device__ __forceinline__ static E* slot(unsigned char* smem, int stage, int j) {
     const unsigned threads = L::kShort ? L::TH : blockDim.x;
-    return reinterpret_cast<E*>(smem + (stage * ALL + BEFORE) * (threads * L::NV * L::V)) +
-           j * threads + threadIdx.x;
+    E* p = reinterpret_cast<E*>(smem + (stage * ALL + BEFORE) * (threads * L::NV * L::V));
+    return L::kShort ? p + j * L::TH + threadIdx.x
+                     : p + ((threadIdx.x >> 5) * L::NV + j) * 32 + (threadIdx.x & 31);
   }
   // Channels past D stay zero in every stage.
   __device__ __forceinline__ static void clear(unsigned char* smem, const Place<L>& at) {
@@ -100,9 +143,13 @@ struct Ring {
 #pragma unroll
     for (int j = 0; j < L::NV; ++j)
       if (at.has(j)) {
-        const E* src = reinterpret_cast<const E*>(p + at.channel(j));
-        if (L::kShort)
-          copy_async(slot(smem, stage, j), src, on ? int(sizeof(E)) : 0);
+        // (an aligned address also where nothing is read: p is row 0 then)
+        const E* src =
+            reinterpret_cast<const E*>(L::kOdd && L::kShort && !on ? p : p + at.channel(j));
+        // a pair past the row's end has one channel, the other is zero
+        const int bytes = L::kOdd && !at.in(j, L::V - 1) ? int(sizeof(T)) : int(sizeof(E));
+        if (L::kShort || L::kOdd)
+          copy_async(slot(smem, stage, j), src, on ? bytes : 0);
         else
           copy_async(slot(smem, stage, j), src);
       }
@@ -112,10 +159,11 @@ struct Ring {
                                               const T* p, int j, const Place<L>& at, bool on) {
     if constexpr (kStages > 0) {
       spread<L, T>(r, *slot(smem, stage, j));
+      if (L::kOdd && at.channel(j) < 0) r[0].v[0] = 0.f;  // the row's before
+    } else if (on) {
+      load_vector<L, T>(r, p, j, at);
     } else {
-      E x{};
-      if (on && at.has(j)) x = load<T, L::V>(p + at.channel(j));
-      spread<L, T>(r, x);
+      spread<L, T>(r, E{});
     }
   }
 };
@@ -126,14 +174,15 @@ __device__ __forceinline__ void copies_wait() {  // for the oldest stage in flig
   asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
 }
 
-// The weights of vector j, `offset` added; ones without any, zeros past D.
+// The weights of vector j, `offset` added; ones without any.  (Channels that are
+// not the row's have inputs of zero, whatever their weight.)
 template <typename L>
 __device__ __forceinline__ void load_weight(F<L::P> (&w)[L::G], const float* p, float offset, int j,
                                             const Place<L>& at) {
 #pragma unroll
   for (int i = 0; i < L::G; ++i) w[i] = all<L::P>(p ? 0.f : 1.f);
   if (p && at.has(j)) {
-    spread<L, float>(w, load<float, L::V>(p + at.channel(j)));
+    load_vector<L, float>(w, p, j, at);
 #pragma unroll
     for (int i = 0; i < L::G; ++i) w[i] = add(w[i], all<L::P>(offset));
   }
@@ -243,16 +292,19 @@ __device__ __forceinline__ void store_partial(float* part, const F<L::P> (&acc)[
   if constexpr (!L::kShort) {
 #pragma unroll
     for (int j = 0; j < L::NV; ++j)
-      if (at.has(j)) store_vector<L, float>(part + at.channel(j), acc[j]);
+#pragma unroll
+      for (int e = 0; e < L::V; ++e)
+        if (at.in(j, e)) part[at.channel(j) + e] = acc[j][e / L::P].v[e % L::P];
   } else {
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < L::NV; ++j)
 #pragma unroll
       for (int e = 0; e < L::V; ++e)
-        smem[at.sub * L::kMost + at.channel(j) + e] = acc[j][e / L::P].v[e % L::P];
+        if (at.in(j, e))
+          smem[at.sub * L::kMost + at.channel(j) + e] = acc[j][e / L::P].v[e % L::P];
     __syncthreads();
-    for (unsigned c = threadIdx.x; c < at.D; c += L::TH) {
+    for (int c = threadIdx.x; c < at.D; c += L::TH) {
       float s = 0.f;
       for (int i = 0; i < L::kRows; ++i) s += smem[i * L::kMost + c];
       part[c] = s;
@@ -262,8 +314,8 @@ __device__ __forceinline__ void store_partial(float* part, const F<L::P> (&acc)[
 
 // Calls f.template run<Layout>() with the layout for rows of D channels: vectors
 // of four where D is a multiple of 4 and every array starts on one (`width` 4: 8
-// bytes of bf16, 16 of fp32), pairs where D is even and they start on one, else
-// single channels.  LONG: vectors of a thread in rows of 257 to 4096 channels.
+// bytes of bf16, 16 of fp32), pairs where they start on one, else single channels.
+// LONG: vectors of a thread in rows of 257 to 4096 channels.
 template <int LONG, typename F>
 int with_layout(int D, int width, F&& f) {
   if (width == 4 && D % 4 == 0) {
@@ -276,11 +328,18 @@ int with_layout(int D, int width, F&& f) {
   }
   if (width >= 2 && D % 2 == 0) {
     if (D <= 32) return f.template run<Layout<8, 256, 2, 2>>();
+    if (D <= 64) return f.template run<Layout<16, 256, 2, 2>>();
     if (D <= 256) return f.template run<Layout<32, 256, 4, 2>>();
     if (D <= 4096) return f.template run<Layout<0, 512, 4, 2>>();
     return f.template run<Layout<0, 512, 16, 2>>();
   }
-  if (D <= 32) return f.template run<Layout<8, 256, 4, 1>>();
+  if (width >= 2) {
+    if (D < 32) return f.template run<Layout<8, 256, 2, 2, true>>();
+    if (D < 64) return f.template run<Layout<16, 256, 2, 2, true>>();
+    if (D < 256) return f.template run<Layout<32, 256, 4, 2, true>>();
+    if (D < 4096) return f.template run<Layout<0, 512, 4, 2, true>>();
+    return f.template run<Layout<0, 512, 17, 2, true>>();
+  }
   if (D <= 256) return f.template run<Layout<32, 256, 8, 1>>();
   if (D <= 4096) return f.template run<Layout<0, 512, 8, 1>>();
   return f.template run<Layout<0, 512, 32, 1>>();

@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(L::TH) gated_norm_kernel(const GatedNormArgs a
         x[j][i] = mul(mul(x[j][i], rstd), w[j][i]);
         if (a.z) x[j][i] = mul(x[j][i], gate(a.act, z[j][i]));
       }
-      if (on && at.has(j)) store_vector<L, T>(static_cast<T*>(a.y) + o + at.channel(j), x[j]);
+      if (on) store_vector<L, T>(static_cast<T*>(a.y) + o, x[j], j, at);
     }
   }
 }
@@ -171,9 +171,9 @@ __global__ void __launch_bounds__(L::TH, L::TH == 512 && L::NV * L::V == 8 ? 2 :
         x[j][i] = mul(rstd, fma(c, x[j][i], mul(dy[j][i], w[j][i])));
         if (a.z) z[j][i] = mul(z[j][i], rstd);
       }
-      if (on && at.has(j)) {
-        store_vector<L, TX>(static_cast<TX*>(a.dx) + o + at.channel(j), x[j]);
-        if (a.z) store_vector<L, T>(static_cast<T*>(a.dz) + o + at.channel(j), z[j]);
+      if (on) {
+        store_vector<L, TX>(static_cast<TX*>(a.dx) + o, x[j], j, at);
+        if (a.z) store_vector<L, T>(static_cast<T*>(a.dz) + o, z[j], j, at);
       }
     }
   }
@@ -193,7 +193,8 @@ struct Forward {
   int run() {
     const int threads = norm_threads<L>(a.D);
     const long long groups = (a.rows + L::kRows - 1) / L::kRows;
-    const int grid = int(std::min<long long>(groups, kForwardThreads / threads * (long long)sms));
+    const int grid =
+        even_grid<L>(std::min<long long>(groups, kForwardThreads / threads * (long long)sms));
     constexpr int kBytes = sizeof(TX) + sizeof(T);
     constexpr size_t kThread = stages<L>(kBytes) * L::NV * L::V * kBytes;
     if (!raise_smem<&gated_norm_kernel<L, TX, T>>(kThread * L::TH)) return GDN_ERR_LAUNCH;
@@ -212,8 +213,8 @@ struct Backward {
     const int threads = norm_threads<L>(a.D);
     const long long groups = (a.rows + L::kRows - 1) / L::kRows;
     const int per_sm = std::max(1, (L::kShort ? 512 : kBackwardThreads) / threads);
-    const int grid = int(std::min({groups, (long long)norm_max_parts(a.rows, a.D),
-                                   (long long)per_sm * sms}));
+    const int grid = even_grid<L>(std::min(
+        {groups, (long long)norm_max_parts(a.rows, a.D), (long long)per_sm * sms}));
     constexpr int kBytes = sizeof(TX) + 2 * sizeof(T);
     constexpr size_t kThread = stages<L>(kBytes) * L::NV * L::V * kBytes;
     if (!raise_smem<&gated_norm_backward_kernel<L, TX, T>>(kThread * L::TH)) return GDN_ERR_LAUNCH;

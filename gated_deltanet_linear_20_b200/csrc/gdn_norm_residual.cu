@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(L::TH) residual_norm_kernel(const ResidualNorm
         r[j][i] = fma(x[j][i], wp[j][i], r[j][i]);
         sq = fma(r[j][i], r[j][i], sq);
       }
-      if (on && at.has(j)) store_vector<L, TR>(static_cast<TR*>(a.r_out) + o + at.channel(j), r[j]);
+      if (on) store_vector<L, TR>(static_cast<TR*>(a.r_out) + o, r[j], j, at);
     }
     float s[1] = {total(sq)};
     row_sum<L, 1>(s, buf, turn);
@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(L::TH) residual_norm_kernel(const ResidualNorm
     for (int j = 0; j < NV; ++j) {
 #pragma unroll
       for (int i = 0; i < G; ++i) r[j][i] = mul(mul(r[j][i], rs), w[j][i]);
-      if (on && at.has(j)) store_vector<L, T>(static_cast<T*>(a.y) + o + at.channel(j), r[j]);
+      if (on) store_vector<L, T>(static_cast<T*>(a.y) + o, r[j], j, at);
     }
   }
 }
@@ -254,9 +254,9 @@ __global__ void __launch_bounds__(L::TH) residual_norm_backward_kernel(const Res
         dwp[j][i] = fma(v[j][i], x[k][i], dwp[j][i]);
         sm = fma(v[j][i], u, sm);
       }
-      if (on && at.has(j)) {
-        store_vector<L, TR>(static_cast<TR*>(a.dr) + o + at.channel(j), q[k]);
-        if (a.z) store_vector<L, T>(static_cast<T*>(a.dz) + o + at.channel(j), z[k]);
+      if (on) {
+        store_vector<L, TR>(static_cast<TR*>(a.dr) + o, q[k], j, at);
+        if (a.z) store_vector<L, T>(static_cast<T*>(a.dz) + o, z[k], j, at);
       }
     }
     if (a.w_post) {
@@ -279,7 +279,7 @@ __global__ void __launch_bounds__(L::TH) residual_norm_backward_kernel(const Res
     }
 #pragma unroll
     for (int j = 0; j < NV; ++j)
-      if (on && at.has(j)) store_vector<L, T>(static_cast<T*>(a.dx) + o + at.channel(j), v[j]);
+      if (on) store_vector<L, T>(static_cast<T*>(a.dx) + o, v[j], j, at);
     if constexpr (kStages > 0) stage = stage == kStages - 1 ? 0 : stage + 1;
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -326,7 +326,8 @@ struct Forward {
   int run() {
     const int threads = norm_threads<L>(a.D);
     const long long groups = (a.rows + L::kRows - 1) / L::kRows;
-    const int grid = int(std::min<long long>(groups, kForwardThreads / threads * (long long)sms));
+    const int grid =
+        even_grid<L>(std::min<long long>(groups, kForwardThreads / threads * (long long)sms));
     constexpr int kBytes = 2 * sizeof(T) + sizeof(TR);
     constexpr size_t kThread = stages<L>(kBytes) * L::NV * L::V * kBytes;
     if (!raise_smem<&residual_norm_kernel<L, T, TR>>(kThread * L::TH)) return GDN_ERR_LAUNCH;
@@ -345,8 +346,8 @@ struct Backward {
     const int threads = norm_threads<L>(a.D);
     const long long groups = (a.rows + L::kRows - 1) / L::kRows;
     const int per_sm = std::max(1, kBackwardThreads / threads);
-    const int grid = int(std::min({groups, (long long)norm_max_parts(a.rows, a.D),
-                                   (long long)per_sm * sms}));
+    const int grid = even_grid<L>(std::min(
+        {groups, (long long)norm_max_parts(a.rows, a.D), (long long)per_sm * sms}));
     constexpr int kBytes = 3 * sizeof(T) + 2 * sizeof(TR);
     constexpr size_t kThread = stages<L>(kBytes) * L::NV * L::V * kBytes;
     if (!raise_smem<&residual_norm_backward_kernel<L, T, TR>>(kThread * L::TH))

@@ -32,7 +32,10 @@ def steps(d, rows, D):
 
 SIZES = [(1, 1), (3, 8), (5, 64), (2, 65), (17, 128), (40, 200), (33, 256), (3, 257), (4, 264),
          (7, 1000), (2, 4096), (3, 4100), (5, 4104), (2, 8192), (2, 9001), (3, 16384), (1, 16383),
-         (1500, 64), (700, 520)]
+         (1500, 64), (700, 520),
+         # odd rows (their pairs are shifted by one) and even ones that are no multiple of 4
+         (37, 33), (300, 257), (301, 63), (9, 4097), (5, 16383), (33, 31), (130, 255), (2, 7),
+         (21, 54), (3, 250), (4, 2770), (3, 16382), (1000, 14)]
 
 
 @pytest.mark.parametrize("z,gate", [(True, "silu"), (True, "sigmoid"), (False, "silu")])
