@@ -67,17 +67,17 @@ __global__ void __launch_bounds__(L::TH) residual_norm_kernel(const ResidualNorm
     const T *px = static_cast<const T*>(a.x) + o, *pz = static_cast<const T*>(a.z) + o;
     const TR* pr = static_cast<const TR*>(a.r) + o;
     F<P> x[NV][G], r[NV][G], z[NV][G];
-    if constexpr (kStages > 0) {
-      copies_wait<kStages>();
-      fetch();  // over the stage before this one
-    }
+    if constexpr (kStages > 0) copies_wait<kStages>();
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       RX::take(x[j], smem, stage, px, j, at, on);
       RR::take(r[j], smem, stage, pr, j, at, on);
       if (a.z) RZ::take(z[j], smem, stage, pz, j, at, on);
     }
-    if constexpr (kStages > 0) stage = stage == kStages - 1 ? 0 : stage + 1;
+    if constexpr (kStages > 0) {
+      stage = stage == kStages - 1 ? 0 : stage + 1;
+      fetch();
+    }
     float rstd = 1.f;
     if (a.w_post) {
       F<P> sq = all<P>(0.f);
@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(L::TH) residual_norm_backward_kernel(const Res
     F<P> x[KV][G], z[KV][G], dy[KV][G], r[KV][G], q[KV][G], v[NV][G];
     if constexpr (kStages > 0) {
       copies_wait<kStages>();
-      fetch();  // over the stage before this one
+      if (!kKeep) fetch();  // over the stage before this one
     }
     const int here = stage;
     // the vectors of the first sum, and those of the second besides
@@ -208,6 +208,7 @@ __global__ void __launch_bounds__(L::TH) residual_norm_backward_kernel(const Res
     if (kKeep) {
 #pragma unroll
       for (int j = 0; j < NV; ++j) take(j, false);
+      if constexpr (kStages > 0) fetch();
     }
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
