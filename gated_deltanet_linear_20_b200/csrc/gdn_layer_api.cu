@@ -11,7 +11,7 @@ using gdn::aligned;
 using gdn::Span;
 
 constexpr long long kMaxTokens = 1LL << 30;
-constexpr long long kMaxElements = 1LL << 40;
+constexpr long long kMaxElements = 1LL << 38;  // more than the device holds
 
 int elem_size(int dtype) { return dtype == GDN_BF16 ? 2 : dtype == GDN_F32 ? 4 : 0; }
 

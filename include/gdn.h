@@ -404,7 +404,8 @@ enum gdn_dtype { GDN_F32 = 0, GDN_BF16 = 1 };
  * status: optional device int, as for gdn_prefill: a bounded device wait that
  * gives up stores GDN_ERR_DEVICE_TIMEOUT there.
  * B*C == 0 is a no-op; T == 0 writes h_T = h0 (or zeros).  Arrays need the
- * alignment of their element type; offsets are 64-bit: B*T up to 2^30 tokens.
+ * alignment of their element type (16 bytes, and rows of a multiple of 16
+ * bytes, make the fast path); offsets are 64-bit: B*T up to 2^30 tokens.
  * Returns GDN_OK after enqueueing, GDN_ERR_NULL, GDN_ERR_ALIGN, GDN_ERR_SHAPE
  * (negative or too large), GDN_ERR_UNSUPPORTED (dtype, device), GDN_ERR_ALIAS
  * (an output overlaps an input or another output, except h_T == h0) or
@@ -435,7 +436,7 @@ int gdn_scan_step(const void* x, const float* g, const void* beta, float* state,
                   int C, int dtype, void* stream);
 
 /* Gradients of gdn_scan's inputs, given those of its outputs:
- *     lam_t = dh_t + exp(g_{t+1}) lam_{t+1},  lam_T = dh_T-th token + dh_T
+ *     lam_t = dh_t + exp(g_{t+1}) lam_{t+1},  lam_T = dh_t at t = T, plus dh_T
  *     dx = beta lam, dbeta = x lam, dg = lam exp(g_t) h_{t-1}, dh0 = exp(g_1) lam_1
  *   x, g, beta, h0 : the forward call's inputs
  *   dh       : [B][T][C] by `dtype`;  dh_T [B][C] fp32 or NULL (zeros)

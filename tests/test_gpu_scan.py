@@ -54,6 +54,9 @@ SIZES = [  # B, T, C: one token, ends inside a slice, a tile, a cluster's tile; 
     (5, 40, 1000), (300, 3, 65), (2, 64, 5000),
     # large enough for TMA, whose boxes reach past channels, sequences and the end
     (3, 100, 1000), (1, 777, 184), (9, 33, 520), (2, 1100, 72), (70, 5, 400),
+    # every launch shape over several tiles: clusters of four warps, one CTA of eight and
+    # of four warps, single warps
+    (1, 1100, 4096), (6, 200, 2560), (20, 70, 2048), (80, 33, 2048),
 ]
 
 
@@ -127,8 +130,9 @@ def test_a_run_of_calls_is_one_sequence():
     ref.assert_within(state, f["h_T"], f["err_T"], F32, "state")
 
 
-def test_invalid_offsets_are_reported_and_leave_outputs_alone():
-    T, C = 60, 66
+@pytest.mark.parametrize("C", [66, 4096])
+def test_invalid_offsets_are_reported_and_leave_outputs_alone(C):
+    T = 60
     d = to_dev(ref.scan_inputs([T], C, F32, seed=6, h0=False))
     for cu, bad in (([0, 20, 10, 60], [1]), ([0, 20, 61, 60], [1, 2]), ([-1, 20, 40, 60], [0])):
         cu_t = torch.tensor(cu, dtype=torch.int32, device=DEV)
@@ -144,18 +148,23 @@ def test_invalid_offsets_are_reported_and_leave_outputs_alone():
         assert gdn.query_status(status) == -3
 
 
-def test_tokens_behind_the_last_sequence_stay():
-    lens, C, T = [20, 13], 64, 50
+@pytest.mark.parametrize("C", [64, 4096])
+def test_tokens_behind_the_last_sequence_stay(C):
+    lens, T = [20, 13], 50
     d = ref.scan_inputs(lens, C, BF, seed=7)
     f = ref.scan(d, lens)
     dd, cu = to_dev(d), offsets(lens)
     pad = lambda t, v: torch.cat([t, torch.full((T - 33, C), v, dtype=t.dtype, device=DEV)])  # noqa: E731
     nan = float("nan")
     h = torch.full((T, C), 3.0, dtype=BF, device=DEV)
-    x, g, b = (pad(dd[k], nan) for k in ("x", "g", "beta"))
-    _, h_T = gdn.scan_varlen(x, g, cu, b, dd["h0"], h=h)
+    x, g, beta = (pad(dd[k], nan) for k in ("x", "g", "beta"))
+    _, h_T = gdn.scan_varlen(x, g, cu, beta, dd["h0"], h=h)
     assert bool((h[33:] == 3.0).all())
     check_forward((h[:33], h_T), f, BF, (33, C), "padded")
+    b = ref.scan_backward(d, lens)
+    got = gdn.scan_varlen_backward(pad(dd["dh"], nan), x, g, cu, beta, dd["h0"],
+                                   dd["dh_T"])
+    check_backward([t[:33] if t.shape[0] == T else t for t in got], b, d, BF, (33, C), "padded")
 
 
 @pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
@@ -251,9 +260,10 @@ def test_repeatable_on_any_stream_and_in_a_graph():
         assert torch.equal(a, b) and torch.equal(a, c)
 
 
-def test_elements_past_32_bits():
+@pytest.mark.parametrize("C", [4096, 4100])
+def test_elements_past_32_bits(C):
     """More than 2^31 elements in one call: the last tokens are right."""
-    T, C = (1 << 19) + 40, 4100
+    T = (1 << 19) + 40
     free, _ = torch.cuda.mem_get_info()
     if free < 40 << 30:
         pytest.skip("needs 40 GB of free device memory")
@@ -267,3 +277,35 @@ def test_elements_past_32_bits():
     f = ref.scan(d, [tail])
     assert not bool(h[0, :-tail].any())
     check_forward((h[:, -tail:], h_T), f, BF, (1, tail, C), "tail")
+
+
+def test_first_calls_inside_a_capture():
+    """A process whose first calls are captured: nothing needs a call before."""
+    import subprocess
+    import sys
+    code = """
+import torch
+import gated_deltanet_linear_20_b200 as gdn
+dev = torch.device('cuda:0')
+x = torch.randn(1, 600, 1024, device=dev).bfloat16()
+g = -torch.rand(1, 600, 1024, device=dev)
+w = torch.ones(1024, device=dev)
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    h, h_T, c = gdn.scan(x, g, save_carries=True)
+    dx = gdn.scan_backward(h, x, g, carries=c)[0]
+    y, r = gdn.residual_norm(h, x, w, w_post=w, scale=w)
+    grads = gdn.residual_norm_backward(dx, None, h, r, w, w_post=w, scale=w)
+    gg = gdn.gated_norm_backward(y, r, w, h)
+graph.replay()
+torch.cuda.synchronize()
+want = gdn.scan(x, g)[0]
+assert torch.equal(h, want)
+assert torch.equal(gg[0], gdn.gated_norm_backward(y, r, w, h)[0])
+print('captured')
+"""
+    import os
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    out = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True,
+                         timeout=300)
+    assert out.returncode == 0 and "captured" in out.stdout, out.stderr[-2000:]
