@@ -16,6 +16,14 @@ row-parallel fp32 kernel; the per-channel-gate prefill runs its own chunked
 tensor-core kernel with Dk = 128 (any Dv); decode at 128 x 128 and 64 x 64 streams the
 state through the decode kernels, at other dims through the row kernel.
 
+Around that layer: the channel recurrence h_t = exp(g_t) h_{t-1} + beta_t x_t
+(``scan``, ``scan_varlen``, ``scan_step`` and their gradients) and the norms
+before and after a block (``gated_norm``, ``residual_norm`` and their gradients):
+
+    h, h_T = scan(x, g, beta, h0)               # x, g, beta [B,T,C]
+    y = gated_norm(o, w, z)                     # per head: o, z [B,T,H,Dv]
+    y, r = residual_norm(x, r, w, w_post=w2)    # r + norm(x), and its norm
+
 The binding is imported lazily so that ``inputs`` (the seeded input
 generator) can be used without loading the CUDA library.
 """

@@ -9,6 +9,12 @@
 // directions.  The backward pass finds rstd and mean(u xh) in one sum over the
 // row (sum x^2 and sum u x), and keeps dw in registers while a CTA walks its
 // rows; the CTAs' partial sums are added by a second launch in a fixed order.
+//
+// Measured (of the measured 6554 GB/s): 524288 x 128 in bf16 67 to 75 us (82 to
+// 91%; half of a run's writes are the one before's, still in L2), its gradient
+// over 131072 x 128 with x in fp32 45 us (79%), of which the first launch takes 34:
+// its bytes at 107% of that rate, a part of the writes being left in L2.  What is
+// left is the second launch and the gap before it.
 #include "gdn_norm.cuh"
 
 namespace gdn {

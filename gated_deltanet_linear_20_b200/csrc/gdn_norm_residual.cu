@@ -12,6 +12,13 @@
 // only inputs in the first sum).  y comes from the fp32 sum before r' is rounded
 // to its type.  The weight gradients of a CTA's rows stay in registers and the
 // CTAs' partial sums are added by a second launch in a fixed order.
+//
+// Measured (of the measured 6554 GB/s): 8192 x 4096 in bf16 48 to 51 us (80 to 86%);
+// gradients of 4096 x 4096 with everything on and r in fp32 75 us (75%), of 8192 x
+// 4096 in bf16 without a gate 98 us (63%).  The gradients are bound by their
+// instructions (67 a channel; a warp issues in half the cycles) and by registers:
+// 24 sums, 24 weights and five inputs of 8 channels a thread leave one CTA of 512
+// threads an SM.
 #include "gdn_norm.cuh"
 
 namespace gdn {

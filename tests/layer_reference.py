@@ -83,9 +83,13 @@ def scan_backward(d, lens):
                 edx=beta.abs() * (el + maglam), edg=edg, edbeta=x.abs() * (el + maglam), edh0=eh0)
 
 
-#: Steps of a bound: expf is off by at most one unit in the last place (two half
-#: steps), the product with the state and the sum by half a step each; a join
-#: adds one exponential and one multiply-add to a run of at least 8 tokens.
+#: Steps of a bound, in half steps of fp32.  A token: the approximate power of two
+#: is off by 2^1.5 (its stated bound of 2^-22.5), the rounding of g log2 e adds
+#: 1.5 |g|, the products with the state and of x with beta and the sum one each on
+#: the magnitudes: at most 5 (1 + |g|) on the decayed state's and 5 on the new
+#: one's.  A join over 16 tokens replaces their 80 + 5 |G| steps by those of one
+#: power, of its product and sum, and of the sum G of their log decays (8 |G|, the
+#: partial sums growing evenly): fewer as long as |G| is below 17.
 STEPS = 5
 
 
