@@ -14,7 +14,7 @@ from typing import Optional
 import torch
 
 from .gdn import _lib
-from .recurrence import _F32, _call, _device, _dtype, _expect, _optional, _out
+from .recurrence import _F32, _begin, _call, _code, _expect, _optional, _out
 
 _vp, _ci, _cz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
 for _name, _args in (
@@ -45,10 +45,10 @@ def _options(eps: float, weight_offset: float, gate: str):
     return ctypes.byref(NormOptions(ctypes.sizeof(NormOptions), eps, weight_offset, code))
 
 
-def _rows(x: torch.Tensor):
-    if x.dim() < 1:
+def _rows(x: torch.Tensor, shape):
+    if len(shape) < 1:
         raise ValueError("x must have at least one dimension")
-    D = x.shape[-1]
+    D = shape[-1]
     return (x.numel() // D if D else 0), D
 
 
@@ -75,17 +75,15 @@ def gated_norm(x: torch.Tensor, w: torch.Tensor, z: Optional[torch.Tensor] = Non
     x [..., D] fp32 or bf16; w [D] fp32; z like x in shape, fp32 or bf16, or None
     (no gate); a is ``gate``: "silu" or "sigmoid".  y has z's type, or without z
     ``out_dtype`` (x's by default)."""
-    dev = _device(x, "gated_norm")
-    rows, D = _rows(x)
-    shape = x.shape
-    xt = _dtype(x, "x")
+    shape, xd, xt, dev = _begin(x, "gated_norm", "")
+    rows, D = _rows(x, shape)
     if out_dtype is None:
-        out_dtype = x.dtype if z is None else z.dtype
-    px = _expect(x, "x", x.dtype, shape, dev)
+        out_dtype = xd if z is None else z.dtype
+    px = _expect(x, "x", xd, shape, dev)
     pw = _expect(w, "w", _F32, (D,), dev)
     pz = _optional(z, "z", out_dtype, shape, dev)
     y = _out(y, "y", out_dtype, shape, dev, x)
-    _call(_lib.gdn_gated_norm, dev, px, xt, pw, pz, y.data_ptr(), rows, D, _dtype(y, "y"),
+    _call(_lib.gdn_gated_norm, dev, px, xt, pw, pz, y.data_ptr(), rows, D, _code(out_dtype, "y"),
           _options(eps, weight_offset, gate))
     return y
 
@@ -96,12 +94,10 @@ def gated_norm_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor,
                         workspace: Optional[torch.Tensor] = None):
     """Gradients of ``gated_norm``: returns (dx, dz, dw), dz None without z.  dx has
     x's type, dz dy's (which is z's), dw [D] is fp32, summed over the rows."""
-    dev = _device(x, "gated_norm_backward")
-    rows, D = _rows(x)
-    shape = x.shape
-    xt = _dtype(x, "x")
-    px = _expect(x, "x", x.dtype, shape, dev)
-    dt = _dtype(dy, "dy")
+    shape, xd, xt, dev = _begin(x, "gated_norm_backward", "")
+    rows, D = _rows(x, shape)
+    px = _expect(x, "x", xd, shape, dev)
+    dt = _code(dy.dtype, "dy")
     pdy = _expect(dy, "dy", dy.dtype, shape, dev)
     pw = _expect(w, "w", _F32, (D,), dev)
     pz = _optional(z, "z", dy.dtype, shape, dev)
@@ -128,18 +124,16 @@ def residual_norm(x: torch.Tensor, r: torch.Tensor, w: torch.Tensor, *,
     x (the block's output), z [..., D] fp32 or bf16; r [..., D] of that type or
     fp32; w, w_post, scale [D] fp32; z, w_post, scale may be None (no gate, no
     norm behind the block, 1).  ``r_out`` may be ``r``."""
-    dev = _device(x, "residual_norm")
-    rows, D = _rows(x)
-    shape = x.shape
-    dt = _dtype(x, "x")
-    px = _expect(x, "x", x.dtype, shape, dev)
-    rt = _dtype(r, "r")
+    shape, xd, dt, dev = _begin(x, "residual_norm", "")
+    rows, D = _rows(x, shape)
+    px = _expect(x, "x", xd, shape, dev)
+    rt = _code(r.dtype, "r")
     pr = _expect(r, "r", r.dtype, shape, dev)
     pw = _expect(w, "w", _F32, (D,), dev)
-    pz = _optional(z, "z", x.dtype, shape, dev)
+    pz = _optional(z, "z", xd, shape, dev)
     pp = _optional(w_post, "w_post", _F32, (D,), dev)
     ps = _optional(scale, "scale", _F32, (D,), dev)
-    y = _out(y, "y", x.dtype, shape, dev, x)
+    y = _out(y, "y", xd, shape, dev, x)
     r_out = _out(r_out, "r_out", r.dtype, shape, dev, r)
     _call(_lib.gdn_residual_norm, dev, px, pr, pw, pz, pp, ps, y.data_ptr(), r_out.data_ptr(), rows,
           D, dt, rt, _options(eps, weight_offset, gate))
@@ -156,17 +150,15 @@ def residual_norm_backward(dy: torch.Tensor, dr_out: Optional[torch.Tensor], x: 
     """Gradients of ``residual_norm`` at the kept sum ``r_out``: returns (dx, dr, dz,
     dw, dw_post, dscale), each None where its input is.  dr_out (of r_out's type,
     None: zeros) is the gradient that reaches r_out from what follows besides y."""
-    dev = _device(x, "residual_norm_backward")
-    rows, D = _rows(x)
-    shape = x.shape
-    dt = _dtype(x, "x")
-    px = _expect(x, "x", x.dtype, shape, dev)
-    rt = _dtype(r_out, "r_out")
+    shape, xd, dt, dev = _begin(x, "residual_norm_backward", "")
+    rows, D = _rows(x, shape)
+    px = _expect(x, "x", xd, shape, dev)
+    rt = _code(r_out.dtype, "r_out")
     pr = _expect(r_out, "r_out", r_out.dtype, shape, dev)
-    pdy = _expect(dy, "dy", x.dtype, shape, dev)
+    pdy = _expect(dy, "dy", xd, shape, dev)
     pdr = _optional(dr_out, "dr_out", r_out.dtype, shape, dev)
     pw = _expect(w, "w", _F32, (D,), dev)
-    pz = _optional(z, "z", x.dtype, shape, dev)
+    pz = _optional(z, "z", xd, shape, dev)
     pp = _optional(w_post, "w_post", _F32, (D,), dev)
     ps = _optional(scale, "scale", _F32, (D,), dev)
     dx, dr, dw = torch.empty_like(x), torch.empty_like(r_out), torch.empty_like(w)

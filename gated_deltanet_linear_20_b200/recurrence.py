@@ -33,10 +33,14 @@ _F32, _I32 = torch.float32, torch.int32
 
 
 def _expect(t, name, dtype, shape, device):
-    """_check with its common answer first: the calls of one token are short."""
-    if type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape and t.device == device \
-            and t.is_contiguous():
-        return t.data_ptr()
+    """_check with its common answer first (the calls of one token are short), and
+    the tensor's address."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == device.index \
+                and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     _check(t, name, dtype, shape, device)
     return t.data_ptr()
 
@@ -45,19 +49,24 @@ def _optional(t, name, dtype, shape, device):
     return None if t is None else _expect(t, name, dtype, shape, device)
 
 
-def _device(t: torch.Tensor, what: str) -> torch.device:
-    if not isinstance(t, torch.Tensor):
-        raise TypeError("x must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{what} runs on CUDA tensors only (no CPU path)")
-    return t.device
-
-
-def _dtype(t: torch.Tensor, name: str) -> int:
-    code = DTYPES.get(t.dtype)
+def _code(dtype: torch.dtype, name: str) -> int:
+    code = DTYPES.get(dtype)
     if code is None:
-        raise TypeError(f"{name} must be torch.float32 or torch.bfloat16, got {t.dtype}")
+        raise TypeError(f"{name} must be torch.float32 or torch.bfloat16, got {dtype}")
     return code
+
+
+def _begin(x: torch.Tensor, what: str, layout: str):
+    """x's shape, type, type code and device; ``layout``: its dimensions, e.g. "[B,C]"
+    ("": any)."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch.Tensor")
+    shape, dtype, device = x.shape, x.dtype, x.device
+    if device.type != "cuda":
+        raise ValueError(f"{what} runs on CUDA tensors only (no CPU path)")
+    if layout and len(shape) != layout.count(",") + 1:
+        raise ValueError(f"x must be {layout}")
+    return shape, dtype, _code(dtype, "x"), device
 
 
 def _call(fn, device: torch.device, *args):
@@ -103,18 +112,14 @@ def scan(x: torch.Tensor, g: torch.Tensor, beta: Optional[torch.Tensor] = None,
     be given preallocated (``h_T`` may be ``h0``).  ``save_carries`` also returns
     the states before every 16th token ([B, ceil(T/16), C] fp32), which
     ``scan_backward`` takes."""
-    dev = _device(x, "scan")
-    if x.dim() != 3:
-        raise ValueError("x must be [B,T,C]")
-    shape = x.shape
+    shape, xt, dt, dev = _begin(x, "scan", "[B,T,C]")
     B, T, C = shape
-    dt = _dtype(x, "x")
-    px = _expect(x, "x", x.dtype, shape, dev)
+    px = _expect(x, "x", xt, shape, dev)
     pg = _expect(g, "g", _F32, shape, dev)
-    pb = _optional(beta, "beta", x.dtype, shape, dev)
+    pb = _optional(beta, "beta", xt, shape, dev)
     p0 = _optional(h0, "h0", _F32, (B, C), dev)
     pst = _optional(status, "status", _I32, (1,), dev)
-    h = _out(h, "h", x.dtype, shape, dev, x)
+    h = _out(h, "h", xt, shape, dev, x)
     h_T = _out(h_T, "h_T", _F32, (B, C), dev)
     carries = torch.empty(_carry_shape(B, B * T, C, False), dtype=_F32, device=dev) \
         if save_carries else None
@@ -123,9 +128,7 @@ def scan(x: torch.Tensor, g: torch.Tensor, beta: Optional[torch.Tensor] = None,
     return (h, h_T, carries) if save_carries else (h, h_T)
 
 
-def _packed(x, cu_seqlens, status, dev):
-    if x.dim() != 2:
-        raise ValueError("x must be [total_T,C]")
+def _packed(cu_seqlens, status, dev):
     if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
         raise ValueError("cu_seqlens must be [N+1]")
     N = cu_seqlens.numel() - 1
@@ -140,16 +143,14 @@ def scan_varlen(x: torch.Tensor, g: torch.Tensor, cu_seqlens: torch.Tensor,
     """``scan`` of N packed sequences: x, g, beta [total_T,C], cu_seqlens int32
     [N+1] on the device, h0 [N,C]; returns (h [total_T,C], h_T [N,C] fp32), and
     with ``save_carries`` the kept states ([total_T // 16 + N, C] fp32)."""
-    dev = _device(x, "scan_varlen")
-    N, pcu, pst = _packed(x, cu_seqlens, status, dev)
-    shape = x.shape
+    shape, xt, dt, dev = _begin(x, "scan_varlen", "[total_T,C]")
     T, C = shape
-    dt = _dtype(x, "x")
-    px = _expect(x, "x", x.dtype, shape, dev)
+    N, pcu, pst = _packed(cu_seqlens, status, dev)
+    px = _expect(x, "x", xt, shape, dev)
     pg = _expect(g, "g", _F32, shape, dev)
-    pb = _optional(beta, "beta", x.dtype, shape, dev)
+    pb = _optional(beta, "beta", xt, shape, dev)
     p0 = _optional(h0, "h0", _F32, (N, C), dev)
-    h = _out(h, "h", x.dtype, shape, dev, x)
+    h = _out(h, "h", xt, shape, dev, x)
     h_T = _out(h_T, "h_T", _F32, (N, C), dev)
     carries = torch.empty(_carry_shape(N, T, C, True), dtype=_F32, device=dev) \
         if save_carries else None
@@ -165,30 +166,25 @@ def scan_step(x: torch.Tensor, g: torch.Tensor, state: torch.Tensor,
     Returns h [B,C], the new state in x's type.
 
     x, beta [B,C] fp32 or bf16 (beta None: 1); g [B,C] fp32."""
-    dev = _device(x, "scan_step")
-    if x.dim() != 2:
-        raise ValueError("x must be [B,C]")
-    shape = x.shape
+    shape, xt, dt, dev = _begin(x, "scan_step", "[B,C]")
     B, C = shape
-    dt = _dtype(x, "x")
-    px = _expect(x, "x", x.dtype, shape, dev)
+    px = _expect(x, "x", xt, shape, dev)
     pg = _expect(g, "g", _F32, shape, dev)
     ps = _expect(state, "state", _F32, shape, dev)
-    pb = _optional(beta, "beta", x.dtype, shape, dev)
-    h = _out(h, "h", x.dtype, shape, dev, x)
+    pb = _optional(beta, "beta", xt, shape, dev)
+    h = _out(h, "h", xt, shape, dev, x)
     _call(_lib.gdn_scan_step, dev, px, pg, pb, ps, h.data_ptr(), B, C, dt)
     return h
 
 
-def _backward(fn, dh, x, g, beta, h0, dh_T, carries, N, tokens, packed, sizes,
-              tail, dev):
-    shape, C = x.shape, x.shape[-1]
-    dt = _dtype(x, "x")
-    px = _expect(x, "x", x.dtype, shape, dev)
+def _backward(fn, dh, x, g, beta, h0, dh_T, carries, N, tokens, packed, sizes, tail, begun):
+    shape, xt, dt, dev = begun
+    C = shape[-1]
+    px = _expect(x, "x", xt, shape, dev)
     pg = _expect(g, "g", _F32, shape, dev)
-    pb = _optional(beta, "beta", x.dtype, shape, dev)
+    pb = _optional(beta, "beta", xt, shape, dev)
     p0 = _optional(h0, "h0", _F32, (N, C), dev)
-    pdh = _expect(dh, "dh", x.dtype, shape, dev)
+    pdh = _expect(dh, "dh", xt, shape, dev)
     pdt = _optional(dh_T, "dh_T", _F32, (N, C), dev)
     kept = carries is not None
     carries = _out(carries, "carries", _F32, _carry_shape(N, tokens, C, packed), dev)
@@ -212,13 +208,11 @@ def scan_backward(dh: torch.Tensor, x: torch.Tensor, g: torch.Tensor,
     dh [B,T,C] has x's type, dh_T [B,C] fp32 or None (zeros).  ``carries`` is what
     ``scan(..., save_carries=True)`` returned for the same inputs; without it the
     states are computed again first."""
-    dev = _device(x, "scan_backward")
-    if x.dim() != 3:
-        raise ValueError("x must be [B,T,C]")
-    B, T, _ = x.shape
-    pst = _optional(status, "status", _I32, (1,), dev)
+    begun = _begin(x, "scan_backward", "[B,T,C]")
+    B, T, _ = begun[0]
+    pst = _optional(status, "status", _I32, (1,), begun[3])
     return _backward(_lib.gdn_scan_backward, dh, x, g, beta, h0, dh_T, carries, B, B * T, False,
-                     (B, T), (pst,), dev)
+                     (B, T), (pst,), begun)
 
 
 def scan_varlen_backward(dh: torch.Tensor, x: torch.Tensor, g: torch.Tensor,
@@ -228,8 +222,8 @@ def scan_varlen_backward(dh: torch.Tensor, x: torch.Tensor, g: torch.Tensor,
                          status: Optional[torch.Tensor] = None):
     """Gradients of ``scan_varlen``'s inputs, as ``scan_backward``.  Gradients of
     tokens behind the last sequence are not written."""
-    dev = _device(x, "scan_varlen_backward")
-    N, pcu, pst = _packed(x, cu_seqlens, status, dev)
-    T = x.shape[0]
+    begun = _begin(x, "scan_varlen_backward", "[total_T,C]")
+    T = begun[0][0]
+    N, pcu, pst = _packed(cu_seqlens, status, begun[3])
     return _backward(_lib.gdn_scan_varlen_backward, dh, x, g, beta, h0, dh_T, carries, N, T, True,
-                     (pcu, N, T), (pst,), dev)
+                     (pcu, N, T), (pst,), begun)
