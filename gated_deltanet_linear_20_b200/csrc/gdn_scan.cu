@@ -50,7 +50,6 @@ using namespace sm100;
 constexpr int kCarryTokens = GDN_SCAN_CARRY_TOKENS;
 constexpr int kMaxCluster = 8;  // CTAs along time
 constexpr uint64_t kWaitLimitNs = 2000000000;  // 2 s: far beyond any legitimate wait
-constexpr long long kTmaElements = 1 << 17;  // of a call, from which TMA is used
 constexpr int kMaxSorted = 128;  // packed sequences that are started longest first
 
 // The map of a run of tokens for V channels: c -> A c + H.  A stays finite, so
@@ -248,11 +247,14 @@ __device__ __forceinline__ void exchange_end(unsigned n, bool late, int* status,
   if (n > 1) cluster_barrier();
 }
 
-// How a slice gets from memory to registers.  By TMA: one lane a warp fetches the
-// warp's slice, S tokens x 32 V channels, one slice ahead; a warp reads only what
-// it fetched, so no barrier is needed.  Else by plain loads.  (Copies by cp.async,
-// each thread its own elements, were slower than either: 32768 x 4096 forward 283
-// us against 207 by TMA; 5 x 577 x 577 in fp32 28 us against 10 by loads.)
+// How a slice gets from memory to registers, one slice ahead of the work on it.
+// Two channels a thread (V = 2): by TMA, one lane a warp fetching the warp's
+// slice, S tokens x 64 channels; a warp reads only what it fetched, so no barrier
+// is needed.  One channel a thread, where TMA cannot go: by loads into registers.
+// (Copies by cp.async, each thread its own elements, were slower than either:
+// 32768 x 4096 forward 283 us against 207 by TMA; 5 x 577 x 577 in fp32 28 us
+// against 10 by loads; loads of pairs, whose registers leave no room for the next
+// slice, 16 x 1024 x 2050 95 us against 74.)
 
 // A tile's slices: the log decays and K arrays of T.
 template <typename T, int V, int S, int W, int K>
@@ -275,32 +277,38 @@ __device__ __forceinline__ void tma_rows(void* dst, const CUtensorMap* map, uint
       : "memory");
 }
 
-// The slice's elements in registers: from the stage (tokens >= cnt of a TMA box
-// are another sequence's: zeros instead), or directly.
-template <bool TMA, typename E, int S>
-__device__ __forceinline__ void take(E (&r)[S], const E (&src)[S][32], const void* p, size_t stride,
-                                     int cnt) {
-  if constexpr (TMA) {
+// The slice's elements from the stage (tokens >= cnt of a TMA box are another
+// sequence's: zeros instead).
+template <typename E, int S>
+__device__ __forceinline__ void take(E (&r)[S], const E (&src)[S][32], int cnt) {
 #pragma unroll
-    for (int i = 0; i < S; ++i) r[i] = src[i][threadIdx.x & 31];
-    if (cnt < S) {
+  for (int i = 0; i < S; ++i) r[i] = src[i][threadIdx.x & 31];
+  if (cnt < S) {
 #pragma unroll
-      for (int i = 0; i < S; ++i)
-        if (i >= cnt) r[i] = E{};
-    }
-  } else {
-    const char* q = static_cast<const char*>(p);
-#pragma unroll
-    for (int i = 0; i < S; ++i) {
-      r[i] = E{};
-      if (i < cnt) r[i] = *reinterpret_cast<const E*>(q + i * stride);
-    }
+    for (int i = 0; i < S; ++i)
+      if (i >= cnt) r[i] = E{};
   }
 }
+// Starts loading them: tokens 0 .. cnt - 1 at p, zeros behind them.
+template <typename E, int S>
+__device__ __forceinline__ void load_slice(E (&r)[S], const void* p, size_t stride, int cnt) {
+  const char* q = static_cast<const char*>(p);
+#pragma unroll
+  for (int i = 0; i < S; ++i) {
+    r[i] = E{};
+    if (i < cnt) r[i] = *reinterpret_cast<const E*>(q + i * stride);
+  }
+}
+template <typename E, int S>
+__device__ __forceinline__ void copy(E (&r)[S], const E (&x)[S]) {
+#pragma unroll
+  for (int i = 0; i < S; ++i) r[i] = x[i];
+}
 
-template <typename T, int V, int S, int W, bool BETA, bool TMA>
+template <typename T, int V, int S, int W, bool BETA>
 __global__ void __launch_bounds__(32 * W, 16 / W)
     scan_kernel(const ScanArgs a, const __grid_constant__ ScanMaps maps) {
+  constexpr bool TMA = V == 2;
   extern __shared__ __align__(128) unsigned char smem[];
   auto& ex = *reinterpret_cast<Exchange<V, W>*>(smem);
   auto& st = *reinterpret_cast<Stage<T, V, S, W, BETA ? 2 : 1>*>(smem + sizeof(Exchange<V, W>));
@@ -320,38 +328,51 @@ __global__ void __launch_bounds__(32 * W, 16 / W)
   if (a.h0) carry = to_f(load<float, V>(a.h0 + (size_t)seq * a.C + c0));
   constexpr int tile = W * S;
   const int step = tile * int(n);
-  const size_t gs = size_t(a.C) * 4, ts = size_t(a.C) * sizeof(T);
+  [[maybe_unused]] const size_t gs = size_t(a.C) * 4, ts = size_t(a.C) * sizeof(T);
   int t0 = int(rank) * tile + w * S, cnt = 0;
-  const char *pg = nullptr, *px = nullptr, *pb = nullptr;  // this thread's slice
   bool late = false;    // a wait ran out: nothing more is fetched or awaited
   unsigned issued = 0;  // slices fetched by TMA
-  // the slice at token t0: tokens past the end are g = x = 0, which leaves the
-  // state as it is; cnt is the same in every lane
+  Vec<float, V> gn[TMA ? 1 : S];  // the next slice, on its way
+  Vec<T, V> xn[TMA ? 1 : S], bn[TMA || !BETA ? 1 : S];
+  // fetches the slice at token t0: tokens past the end are g = x = 0, which leaves
+  // the state as it is; cnt is the same in every lane
   const auto place = [&] {
     cnt = min(max(s.len - t0, 0), S);
-    const size_t at = cnt > 0 ? size_t(s.start + t0) * a.C + c0 : 0;
-    pg = reinterpret_cast<const char*>(a.g + at);
-    px = reinterpret_cast<const char*>(static_cast<const T*>(a.x) + at);
-    if (BETA) pb = reinterpret_cast<const char*>(static_cast<const T*>(a.beta) + at);
-    if (TMA && cnt > 0 && !late) ++issued;
-    if (TMA && cnt > 0 && !late && lane == 0) {
-      const int c = (id % a.cblocks) * 32 * V, row = int(s.start) + t0;
-      mbar_arrive_expect_tx(smem_u32(&ex.full[w]), sizeof(st.g[w]) + (BETA ? 2 : 1) * sizeof(st.t[0][w]));
-      tma_rows(&st.g[w], &maps.g, &ex.full[w], c, row);
-      tma_rows(&st.t[0][w], &maps.t[0], &ex.full[w], c, row);
-      if (BETA) tma_rows(&st.t[BETA ? 1 : 0][w], &maps.t[1], &ex.full[w], c, row);
+    if constexpr (TMA) {
+      if (cnt > 0 && !late) {
+        ++issued;
+        if (lane == 0) {
+          const int c = (id % a.cblocks) * 32 * V, row = int(s.start) + t0;
+          mbar_arrive_expect_tx(smem_u32(&ex.full[w]),
+                                sizeof(st.g[w]) + (BETA ? 2 : 1) * sizeof(st.t[0][w]));
+          tma_rows(&st.g[w], &maps.g, &ex.full[w], c, row);
+          tma_rows(&st.t[0][w], &maps.t[0], &ex.full[w], c, row);
+          if (BETA) tma_rows(&st.t[BETA ? 1 : 0][w], &maps.t[1], &ex.full[w], c, row);
+        }
+      }
+    } else {
+      const size_t at = cnt > 0 ? size_t(s.start + t0) * a.C + c0 : 0;
+      load_slice(gn, a.g + at, gs, cnt);
+      load_slice(xn, static_cast<const T*>(a.x) + at, ts, cnt);
+      if constexpr (BETA) load_slice(bn, static_cast<const T*>(a.beta) + at, ts, cnt);
     }
   };
   if (s.len > 0) place();
   int round = 0;
   for (int base = 0; base < s.len; base += step, ++round) {
-    if (TMA && cnt > 0) mbar_wait_warp(smem_u32(&ex.full[w]), (issued - 1) & 1, &late, kWaitLimitNs);
     Vec<float, V> g[S];
-    Vec<T, V> x[S], b[S];
-    take<TMA>(g, st.g[w], pg, gs, cnt);
-    take<TMA>(x, st.t[0][w], px, ts, cnt);
-    if (BETA) take<TMA>(b, st.t[BETA ? 1 : 0][w], pb, ts, cnt);
-    if (TMA) __syncwarp();  // the next fetch overwrites what every lane has taken
+    Vec<T, V> x[S], b[BETA ? S : 1];
+    if constexpr (TMA) {
+      if (cnt > 0) mbar_wait_warp(smem_u32(&ex.full[w]), (issued - 1) & 1, &late, kWaitLimitNs);
+      take(g, st.g[w], cnt);
+      take(x, st.t[0][w], cnt);
+      if constexpr (BETA) take(b, st.t[1][w], cnt);
+      __syncwarp();  // the next fetch overwrites what every lane has taken
+    } else {
+      copy(g, gn);
+      copy(x, xn);
+      if constexpr (BETA) copy(b, bn);
+    }
     const int now = t0, have = cnt;
     t0 += step;
     if (base + step < s.len) place();  // in flight while this slice is worked on
@@ -360,7 +381,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W)
 #pragma unroll
     for (int i = 0; i < S; ++i) {
       al[i] = decay(to_f(g[i]));
-      u[i] = BETA ? mul(to_f(x[i]), to_f(b[i])) : to_f(x[i]);
+      u[i] = BETA ? mul(to_f(x[i]), to_f(b[BETA ? i : 0])) : to_f(x[i]);
       m.A = add(m.A, to_f(g[i]));
       m.H = fma(al[i], m.H, u[i]);
     }
@@ -394,9 +415,10 @@ __global__ void __launch_bounds__(32 * W, 16 / W)
 // boundary is mu_t = alpha_t lam_t.  h_{t-1} is rebuilt in 32 bits from the
 // states that the forward pass kept every 16 tokens: reading them costs 4/16
 // byte an element, reading h itself 2 to 4 and, in bf16, its rounding in dg.
-template <typename T, int V, int S, int W, bool BETA, bool TMA>
+template <typename T, int V, int S, int W, bool BETA>
 __global__ void __launch_bounds__(32 * W, 16 / W)
     scan_backward_kernel(const ScanBackwardArgs a, const __grid_constant__ ScanMaps maps) {
+  constexpr bool TMA = V == 2;
   // the later slices of a kept state's 16 tokens start from the slices before
   constexpr int M = kCarryTokens / S;
   extern __shared__ __align__(128) unsigned char smem[];
@@ -422,29 +444,36 @@ __global__ void __launch_bounds__(32 * W, 16 / W)
   constexpr int tile = W * S;
   const int tiles = (s.len + tile - 1) / tile;
   const int sw = W - 1 - w;  // scan order runs backwards in time
-  const size_t gs = size_t(f.C) * 4, ts = size_t(f.C) * sizeof(T);
+  [[maybe_unused]] const size_t gs = size_t(f.C) * 4, ts = size_t(f.C) * sizeof(T);
   int ti = tiles - 1 - int(rank), cnt = 0;  // the tile; below 0: past the start
-  const char *pg = nullptr, *pd = nullptr, *px = nullptr, *pb = nullptr;
   size_t at = 0;
   Vec<float, V> kept{};
   bool late = false;
   unsigned issued = 0;
+  Vec<float, V> gn[TMA ? 1 : S];
+  Vec<T, V> dn[TMA ? 1 : S], xn[TMA ? 1 : S], bn[TMA || !BETA ? 1 : S];
   const auto place = [&] {
     const int t0 = ti * tile + sw * S;
     cnt = ti >= 0 ? min(max(s.len - t0, 0), S) : 0;
     at = cnt > 0 ? size_t(s.start + t0) * f.C + c0 : 0;
-    pg = reinterpret_cast<const char*>(f.g + at);
-    pd = reinterpret_cast<const char*>(static_cast<const T*>(a.dh) + at);
-    px = reinterpret_cast<const char*>(static_cast<const T*>(f.x) + at);
-    if (BETA) pb = reinterpret_cast<const char*>(static_cast<const T*>(f.beta) + at);
-    if (TMA && cnt > 0 && !late) ++issued;
-    if (TMA && cnt > 0 && !late && lane == 0) {
-      const int c = (id % f.cblocks) * 32 * V, row = int(s.start) + t0;
-      mbar_arrive_expect_tx(smem_u32(&ex.full[w]), sizeof(st.g[w]) + (BETA ? 3 : 2) * sizeof(st.t[0][w]));
-      tma_rows(&st.g[w], &maps.g, &ex.full[w], c, row);
-      tma_rows(&st.t[0][w], &maps.t[0], &ex.full[w], c, row);
-      tma_rows(&st.t[1][w], &maps.t[1], &ex.full[w], c, row);
-      if (BETA) tma_rows(&st.t[BETA ? 2 : 0][w], &maps.t[2], &ex.full[w], c, row);
+    if constexpr (TMA) {
+      if (cnt > 0 && !late) {
+        ++issued;
+        if (lane == 0) {
+          const int c = (id % f.cblocks) * 32 * V, row = int(s.start) + t0;
+          mbar_arrive_expect_tx(smem_u32(&ex.full[w]),
+                                sizeof(st.g[w]) + (BETA ? 3 : 2) * sizeof(st.t[0][w]));
+          tma_rows(&st.g[w], &maps.g, &ex.full[w], c, row);
+          tma_rows(&st.t[0][w], &maps.t[0], &ex.full[w], c, row);
+          tma_rows(&st.t[1][w], &maps.t[1], &ex.full[w], c, row);
+          if (BETA) tma_rows(&st.t[BETA ? 2 : 0][w], &maps.t[2], &ex.full[w], c, row);
+        }
+      }
+    } else {
+      load_slice(gn, f.g + at, gs, cnt);
+      load_slice(dn, static_cast<const T*>(a.dh) + at, ts, cnt);
+      load_slice(xn, static_cast<const T*>(f.x) + at, ts, cnt);
+      if constexpr (BETA) load_slice(bn, static_cast<const T*>(f.beta) + at, ts, cnt);
     }
     if (cnt > 0)
       kept = load<float, V>(f.carries + size_t(s.carry_row + t0 / kCarryTokens) * f.C + c0);
@@ -453,20 +482,29 @@ __global__ void __launch_bounds__(32 * W, 16 / W)
   int round = 0;
   for (int first = 0; first < tiles; first += int(n), ++round) {
     const int set = round & 1;
-    if (TMA && cnt > 0) mbar_wait_warp(smem_u32(&ex.full[w]), (issued - 1) & 1, &late, kWaitLimitNs);
     Vec<float, V> g[S];
-    Vec<T, V> x[S], b[S], d[S];
-    take<TMA>(g, st.g[w], pg, gs, cnt);
-    take<TMA>(d, st.t[0][w], pd, ts, cnt);
-    take<TMA>(x, st.t[1][w], px, ts, cnt);
-    if (BETA) take<TMA>(b, st.t[BETA ? 2 : 0][w], pb, ts, cnt);
-    if (TMA) __syncwarp();
+    Vec<T, V> x[S], b[BETA ? S : 1], d[S];
+    if constexpr (TMA) {
+      if (cnt > 0) mbar_wait_warp(smem_u32(&ex.full[w]), (issued - 1) & 1, &late, kWaitLimitNs);
+      take(g, st.g[w], cnt);
+      take(d, st.t[0][w], cnt);
+      take(x, st.t[1][w], cnt);
+      if constexpr (BETA) take(b, st.t[2][w], cnt);
+      __syncwarp();
+    } else {
+      copy(g, gn);
+      copy(d, dn);
+      copy(x, xn);
+      if constexpr (BETA) copy(b, bn);
+    }
     F<V> h = to_f(kept), mu;
     const size_t out = at;
     const int have = cnt;
     ti -= int(n);
     if (first + int(n) < tiles) place();
-    const auto input = [&](int i) { return BETA ? mul(to_f(x[i]), to_f(b[i])) : to_f(x[i]); };
+    const auto input = [&](int i) {
+      return BETA ? mul(to_f(x[i]), to_f(b[BETA ? i : 0])) : to_f(x[i]);
+    };
     F<V> al[S];
     Map<V> m{}, mf{};
 #pragma unroll
@@ -497,7 +535,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W)
       mu = mul(al[i], lam);
       if (on && i < have) {
         const size_t o = out + (size_t)i * f.C;
-        store<T, V>(static_cast<T*>(a.dx) + o, (BETA ? mul(lam, to_f(b[i])) : lam).v);
+        store<T, V>(static_cast<T*>(a.dx) + o, (BETA ? mul(lam, to_f(b[BETA ? i : 0])) : lam).v);
         store<float, V>(a.dg + o, mul(mu, hp[i]).v);
         if (BETA) store<T, V>(static_cast<T*>(a.dbeta) + o, mul(lam, to_f(x[i])).v);
       }
@@ -557,19 +595,13 @@ Shape pick_shape(const ScanArgs& a, int S, long long chains, int sms, int few) {
   return {W, n};
 }
 
-// go(warps, has beta, by TMA), all as types.  Odd channel counts have four or eight
-// warps and no TMA.
-template <int V, int FEW, typename Go>
-bool dispatch_scan(int warps, bool beta, bool tma, Go&& go) {
-  const auto with = [&](auto w, auto b) {
-    if constexpr (V == 2)
-      if (tma) return go(w, b, std::true_type{});
-    return go(w, b, std::false_type{});
-  };
+// go(warps, has beta), both as types.
+template <int FEW, typename Go>
+bool dispatch_scan(int warps, bool beta, Go&& go) {
   const auto sized = [&](auto w) {
-    return beta ? with(w, std::true_type{}) : with(w, std::false_type{});
+    return beta ? go(w, std::true_type{}) : go(w, std::false_type{});
   };
-  if constexpr (V == 2)
+  if constexpr (FEW < 4)
     if (warps == FEW) return sized(std::integral_constant<int, FEW>{});
   if (warps == 8) return sized(std::integral_constant<int, 8>{});
   return sized(std::integral_constant<int, 4>{});
@@ -593,24 +625,13 @@ bool launch_cluster(const Args& args, const ScanMaps& maps, int threads, size_t 
   return cudaLaunchKernelEx(&cfg, Kernel, args, maps) == cudaSuccess;
 }
 
-// TMA wants 16-byte rows and bases.  Encoding its maps takes the host some tenths
-// of a microsecond, which calls of 64 x 2048 elements and more win back (16 x 2048:
-// 5.4 us a call against 5.2, 128 x 2048: 6.4 against 6.5; backward 6.2 against 6.1
-// and 6.5 against 7.0).
-bool tma_ok(const ScanArgs& a, long long rows, int esize, std::initializer_list<const void*> ins) {
-  if (a.C < 64 || a.C * esize % 16 != 0 || rows * a.C < kTmaElements) return false;
-  for (const void* p : ins)
-    if (!aligned(p, 16)) return false;
-  return aligned(a.g, 16);
-}
-
 // The shape of a launch, its channel blocks and the order of its sequences.
 template <int V>
 bool plan(ScanArgs& a, int S, int few, int sms, long long* chains, Shape* shape) {
   a.cblocks = (a.C + 32 * V - 1) / (32 * V);
   *chains = (long long)a.cblocks * a.N;
   if (*chains * kMaxCluster > 0x7fffffffLL) return false;
-  *shape = pick_shape(a, S, *chains, sms, V == 2 ? few : 4);
+  *shape = pick_shape(a, S, *chains, sms, few);
   a.sorted = a.cu_seqlens && a.N <= kMaxSorted && shape->warps >= 4 &&
              *chains * shape->cluster > 16 / shape->warps * (long long)sms;
   return true;
@@ -618,92 +639,91 @@ bool plan(ScanArgs& a, int S, int few, int sms, long long* chains, Shape* shape)
 
 template <typename T, int V, int S>
 int run_scan(ScanArgs a, int sms, cudaStream_t stream) {
+  constexpr int kFew = V == 2 ? 1 : 4;
   long long chains;
   Shape sh;
-  if (!plan<V>(a, S, 1, sms, &chains, &sh)) return GDN_ERR_SHAPE;
+  if (!plan<V>(a, S, kFew, sms, &chains, &sh)) return GDN_ERR_SHAPE;
   const long long rows = a.cu_seqlens ? a.T : (long long)a.N * a.T;
   constexpr bool bf16 = sizeof(T) == 2;
   ScanMaps maps{};
-  bool tma = V == 2 && tma_ok(a, rows, sizeof(T), {a.x, a.beta});
-  if (tma)
-    tma = encode_rows(&maps.g, a.g, rows, a.C, 64, S, false) &&
-          encode_rows(&maps.t[0], a.x, rows, a.C, 64, S, bf16) &&
-          (!a.beta || encode_rows(&maps.t[1], a.beta, rows, a.C, 64, S, bf16));
-  const auto go = [&](auto warps, auto beta, auto by_tma) {
+  if (V == 2 && rows > 0 &&
+      !(encode_rows(&maps.g, a.g, rows, a.C, 64, S, false) &&
+        encode_rows(&maps.t[0], a.x, rows, a.C, 64, S, bf16) &&
+        (!a.beta || encode_rows(&maps.t[1], a.beta, rows, a.C, 64, S, bf16))))
+    return GDN_ERR_LAUNCH;
+  const auto go = [&](auto warps, auto beta) {
     constexpr int W = decltype(warps)::value;
-    constexpr bool kBeta = decltype(beta)::value, kTma = decltype(by_tma)::value;
+    constexpr bool kBeta = decltype(beta)::value;
     constexpr size_t smem =
-        sizeof(Exchange<V, W>) + (kTma ? sizeof(Stage<T, V, S, W, kBeta ? 2 : 1>) : 0);
-    return launch_cluster<&scan_kernel<T, V, S, W, kBeta, kTma>>(a, maps, 32 * W, smem, chains,
-                                                                  sh.cluster, stream);
+        sizeof(Exchange<V, W>) + (V == 2 ? sizeof(Stage<T, V, S, W, kBeta ? 2 : 1>) : 0);
+    return launch_cluster<&scan_kernel<T, V, S, W, kBeta>>(a, maps, 32 * W, smem, chains,
+                                                           sh.cluster, stream);
   };
-  return dispatch_scan<V, 1>(sh.warps, a.beta != nullptr, tma, go) ? GDN_OK : GDN_ERR_LAUNCH;
+  return dispatch_scan<kFew>(sh.warps, a.beta != nullptr, go) ? GDN_OK : GDN_ERR_LAUNCH;
 }
 
 template <typename T, int V, int S>
 int run_backward(ScanBackwardArgs a, int sms, cudaStream_t stream) {
+  constexpr int kFew = V == 2 ? kCarryTokens / S : 4;
+  static_assert(kFew * S % kCarryTokens == 0, "a tile starts at a kept state");
   ScanArgs& f = a.f;
   long long chains;
   Shape sh;
-  constexpr int kFew = kCarryTokens / S;  // a tile starts at a kept state
   if (!plan<V>(f, S, kFew, sms, &chains, &sh)) return GDN_ERR_SHAPE;
   const long long rows = f.cu_seqlens ? f.T : (long long)f.N * f.T;
   constexpr bool bf16 = sizeof(T) == 2;
   ScanMaps maps{};
-  bool tma = V == 2 && tma_ok(f, rows, sizeof(T), {f.x, f.beta, a.dh});
-  if (tma)
-    tma = encode_rows(&maps.g, f.g, rows, f.C, 64, S, false) &&
-          encode_rows(&maps.t[0], a.dh, rows, f.C, 64, S, bf16) &&
-          encode_rows(&maps.t[1], f.x, rows, f.C, 64, S, bf16) &&
-          (!f.beta || encode_rows(&maps.t[2], f.beta, rows, f.C, 64, S, bf16));
-  const auto go = [&](auto warps, auto beta, auto by_tma) {
+  if (V == 2 && rows > 0 &&
+      !(encode_rows(&maps.g, f.g, rows, f.C, 64, S, false) &&
+        encode_rows(&maps.t[0], a.dh, rows, f.C, 64, S, bf16) &&
+        encode_rows(&maps.t[1], f.x, rows, f.C, 64, S, bf16) &&
+        (!f.beta || encode_rows(&maps.t[2], f.beta, rows, f.C, 64, S, bf16))))
+    return GDN_ERR_LAUNCH;
+  const auto go = [&](auto warps, auto beta) {
     constexpr int W = decltype(warps)::value;
-    constexpr bool kBeta = decltype(beta)::value, kTma = decltype(by_tma)::value;
+    constexpr bool kBeta = decltype(beta)::value;
     constexpr size_t smem = sizeof(Exchange<V, W>) + sizeof(Map<V>[2][W][32]) +
-                            (kTma ? sizeof(Stage<T, V, S, W, kBeta ? 3 : 2>) : 0);
-    return launch_cluster<&scan_backward_kernel<T, V, S, W, kBeta, kTma>>(
-        a, maps, 32 * W, smem, chains, sh.cluster, stream);
+                            (V == 2 ? sizeof(Stage<T, V, S, W, kBeta ? 3 : 2>) : 0);
+    return launch_cluster<&scan_backward_kernel<T, V, S, W, kBeta>>(a, maps, 32 * W, smem, chains,
+                                                                    sh.cluster, stream);
   };
-  return dispatch_scan<V, kFew>(sh.warps, f.beta != nullptr, tma, go) ? GDN_OK : GDN_ERR_LAUNCH;
+  return dispatch_scan<kFew>(sh.warps, f.beta != nullptr, go) ? GDN_OK : GDN_ERR_LAUNCH;
 }
 
-// Two channels a thread where the channel count is even and every array starts
-// on a pair (4 bytes of bf16, 8 of fp32); else one.
-bool pairs_ok(const ScanArgs& a, int esize) {
-  const auto ok = [](const void* p, uintptr_t m) {
-    return (reinterpret_cast<uintptr_t>(p) & (m - 1)) == 0;
+// Two channels a thread and TMA: rows of 64 channels or more, inputs whose rows and
+// bases are multiples of 16 bytes, outputs and states that start on a pair.
+// Encoding the maps takes the host some tenths of a microsecond (16 x 2048: 5.4 us
+// a call against 5.2 with loads, 128 x 2048: 6.4 against 6.5, backward 6.2 against
+// 6.1 and 6.5 against 7.0).
+bool wide_ok(int C, int esize, std::initializer_list<const void*> in,
+             std::initializer_list<const void*> out, std::initializer_list<const void*> f32) {
+  if (C < 64 || C * (long long)esize % 16 != 0) return false;
+  const auto all = [](std::initializer_list<const void*> v, uintptr_t n) {
+    return std::all_of(v.begin(), v.end(), [n](const void* p) { return aligned(p, n); });
   };
-  const uintptr_t e2 = 2 * uintptr_t(esize);
-  return a.C % 2 == 0 && ok(a.x, e2) && ok(a.beta, e2) && ok(a.h, e2) && ok(a.g, 8) &&
-         ok(a.h0, 8) && ok(a.h_T, 8) && ok(a.carries, 8);
+  return all(in, 16) && all(out, 2 * uintptr_t(esize)) && all(f32, 8);
 }
 
 }  // namespace
 
 int launch_scan(const ScanArgs& a, int dtype, int sms, cudaStream_t stream) {
-  const bool pairs = pairs_ok(a, dtype == GDN_BF16 ? 2 : 4);
+  const int e = dtype == GDN_BF16 ? 2 : 4;
+  const bool wide = wide_ok(a.C, e, {a.x, a.g, a.beta}, {a.h}, {a.h0, a.h_T, a.carries});
   if (dtype == GDN_BF16)
-    return pairs ? run_scan<__nv_bfloat16, 2, 16>(a, sms, stream)
-                 : run_scan<__nv_bfloat16, 1, 16>(a, sms, stream);
-  return pairs ? run_scan<float, 2, 8>(a, sms, stream) : run_scan<float, 1, 16>(a, sms, stream);
+    return wide ? run_scan<__nv_bfloat16, 2, 16>(a, sms, stream)
+                : run_scan<__nv_bfloat16, 1, 16>(a, sms, stream);
+  return wide ? run_scan<float, 2, 8>(a, sms, stream) : run_scan<float, 1, 16>(a, sms, stream);
 }
 
 int launch_scan_backward(const ScanBackwardArgs& a, int dtype, int sms, cudaStream_t stream) {
-  const int esize = dtype == GDN_BF16 ? 2 : 4;
-  ScanArgs o{};  // the arrays of the backward pass alone, for the same rule
-  o.C = a.f.C;
-  o.x = a.dh;
-  o.beta = a.dx;
-  o.h = a.dbeta;
-  o.g = a.dg;
-  o.h0 = a.dh_T;
-  o.h_T = a.dh0;
-  const bool pairs = pairs_ok(a.f, esize) && pairs_ok(o, esize);
+  const int e = dtype == GDN_BF16 ? 2 : 4;
+  const bool wide = wide_ok(a.f.C, e, {a.f.x, a.f.g, a.f.beta, a.dh}, {a.dx, a.dbeta},
+                            {a.dg, a.dh_T, a.dh0, a.f.carries});
   if (dtype == GDN_BF16)
-    return pairs ? run_backward<__nv_bfloat16, 2, 8>(a, sms, stream)
-                 : run_backward<__nv_bfloat16, 1, 16>(a, sms, stream);
-  return pairs ? run_backward<float, 2, 8>(a, sms, stream)
-               : run_backward<float, 1, 16>(a, sms, stream);
+    return wide ? run_backward<__nv_bfloat16, 2, 8>(a, sms, stream)
+                : run_backward<__nv_bfloat16, 1, 8>(a, sms, stream);
+  return wide ? run_backward<float, 2, 8>(a, sms, stream)
+              : run_backward<float, 1, 8>(a, sms, stream);
 }
 
 template <typename T, int V>
