@@ -570,10 +570,13 @@ __global__ void __launch_bounds__(256) scan_step_kernel(const T* x, const float*
 // resident at 128 registers.  In microseconds, forward / backward, at bf16 with beta:
 //   few     (one 16-token slice, or chains enough to fill the GPU one warp each)
 //           64 x 16 x 4096: 12 / 19 against 24 / 27 on four warps
-//   8, n=1  packed sequences, whose longest bound the launch: 32 of 512 tokens on
-//           average, 2048 channels, 51 / 107 against 56 / 134 on four warps;
-//           1.5 to 4 chains an SM: 8 x 2048 x 2048 56 / 111, four warps on two
-//           CTAs 59 / 126
+//   packed  sequences end at different times, so more CTAs are started than are
+//           resident.  8 sequences, 8192 x 2048 (256 chains): 38 / 68 on clusters of
+//           4, 45 / 96 on 2, 45 / 70 on 8; 64, 32768 x 512 (512 chains): 46 / 71, 45
+//           / 93, 65 / 91.  32, 16384 x 2048 (1024 chains): 58 / 107 on one CTA of
+//           eight warps, 64 / 112 on two of four, 80 / 129 on four
+//   8, n=1  1.5 to 4 chains an SM: 8 x 2048 x 2048 56 / 111, four warps on two CTAs
+//           59 / 126
 //   4, n    else as many CTAs as are resident at once: 4 x 4096 x 2048 86 / 190 on
 //           1, 62 / 137 on 2, 58 / 108 on 4, 62 / 112 on 8 (two waves)
 //   8, n=8  so few chains that even this is resident: 4096 x 2048 20 / 35 against
@@ -583,15 +586,21 @@ struct Shape {
   int warps, cluster;
 };
 Shape pick_shape(const ScanArgs& a, int S, long long chains, int sms, int few) {
+  const bool packed = a.cu_seqlens && a.N > 1;
   const long long len = a.cu_seqlens ? std::max<long long>(1, a.T / std::max(1, a.N)) : a.T;
   if (len <= few * S || chains >= 16LL * sms) return {few, 1};
   const auto resident = [&](int warps) { return 16 / warps * (long long)sms * 9 / 10; };
   int W = 4;
-  if (len > 4 * S && (a.cu_seqlens || (2 * chains >= 3LL * sms && chains <= 4LL * sms) ||
-                      chains * kMaxCluster <= resident(8)))
+  if (len > 4 * S && (packed ? 4 * chains > 14LL * sms
+                             : (2 * chains >= 3LL * sms && chains <= 4LL * sms) ||
+                                   chains * kMaxCluster <= resident(8)))
     W = 8;
   int n = 1;
-  while (n < kMaxCluster && chains * n * 2 <= resident(W) && (long long)n * W * S < len) n *= 2;
+  if (packed)
+    n = W == 8 ? 1 : 8 * chains <= 4LL * sms ? 8 : 4;
+  else
+    while (n < kMaxCluster && chains * n * 2 <= resident(W)) n *= 2;
+  while (n > 1 && (n / 2) * (long long)W * S >= len) n /= 2;  // each CTA has tokens
   return {W, n};
 }
 
