@@ -17,8 +17,8 @@
 // in registers), the W warps of a CTA own consecutive slices, and the CTAs of a
 // cluster consecutive tiles of W S tokens; the cluster walks its sequence
 // cluster-tile by cluster-tile.  Per cluster-tile each thread (1) takes its slice
-// from shared memory, where TMA has put it, starts the fetch of the next one and
-// finds its map, (2) leaves it in shared memory, where the CTA's map is composed
+// (from shared memory, where TMA has put it, or from registers that plain loads have
+// filled), starts the fetch of the next one and finds its map, (2) leaves it in shared memory, where the CTA's map is composed
 // and sent to the other CTAs of the cluster, (3) applies the maps before its own
 // to the carried state and (4) walks its slice again from the right state,
 // writing results.  Each element is read once and written once, no global memory
@@ -203,7 +203,8 @@ __device__ __forceinline__ void scan_exchange(Exchange<V, W>& ex, int round, con
                                               unsigned rank, unsigned n, bool* late) {
   const int set = round & 1;
   ex.warp[set][w][lane] = mine;
-  if (n > 1 && threadIdx.x == 0 && !*late) mbar_arrive_expect_tx(smem_u32(&ex.bar[set]), n * 32 * sizeof(Map<V>));
+  if (n > 1 && threadIdx.x == 0 && !*late)
+    mbar_arrive_expect_tx(smem_u32(&ex.bar[set]), n * 32 * sizeof(Map<V>));
   __syncthreads();
   c = carry;
   if (n > 1) {
@@ -323,9 +324,9 @@ __global__ void __launch_bounds__(32 * W, 16 / W)
     if (a.status && threadIdx.x == 0 && rank == 0) *a.status = GDN_ERR_SHAPE;
     return;
   }
-  exchange_init(ex, n, TMA);
-  F<V> carry{};
+  F<V> carry{};  // (read ahead of the barrier: h_T may be h0, and one CTA writes it)
   if (a.h0) carry = to_f(load<float, V>(a.h0 + (size_t)seq * a.C + c0));
+  exchange_init(ex, n, TMA);
   constexpr int tile = W * S;
   const int step = tile * int(n);
   [[maybe_unused]] const size_t gs = size_t(a.C) * 4, ts = size_t(a.C) * sizeof(T);
@@ -438,9 +439,9 @@ __global__ void __launch_bounds__(32 * W, 16 / W)
     if (f.status && threadIdx.x == 0 && rank == 0) *f.status = GDN_ERR_SHAPE;
     return;
   }
-  exchange_init(ex, n, TMA);
   F<V> carry{};
   if (a.dh_T) carry = to_f(load<float, V>(a.dh_T + (size_t)seq * f.C + c0));
+  exchange_init(ex, n, TMA);
   constexpr int tile = W * S;
   const int tiles = (s.len + tile - 1) / tile;
   const int sw = W - 1 - w;  // scan order runs backwards in time

@@ -111,6 +111,22 @@ def test_scan_step(B, C, beta, dtype):
     ref.assert_within(state, f["h_T"], f["err_T"], F32, "state")
 
 
+@pytest.mark.parametrize("B,T,C", [(1, 300, 64), (1, 500, 4096), (4, 200, 63), (20, 70, 2048), (3, 1, 65)])
+def test_states_in_place_are_those_of_separate_ones(B, T, C):
+    d = to_dev(ref.scan_inputs([T] * B, C, BF, seed=T + C))
+    bt = batch(d, B, T)
+    h, h_T = gdn.scan(bt["x"], bt["g"], bt["beta"], bt["h0"])
+    cu = offsets([T] * B)
+    for _ in range(20):
+        s = d["h0"].clone()
+        got, out = gdn.scan(bt["x"], bt["g"], bt["beta"], s, h_T=s)
+        assert out is s and torch.equal(s, h_T) and torch.equal(got, h)
+        s = d["h0"].clone()
+        gdn.scan_varlen(d["x"], d["g"], cu, d["beta"], s, h_T=s)
+        want = gdn.scan_varlen(d["x"], d["g"], cu, d["beta"], d["h0"])[1]
+        assert torch.equal(s, want)
+
+
 def test_a_run_of_calls_is_one_sequence():
     """Prefill in two calls, then single tokens, the state carried in place."""
     T, C, cut, steps = 300, 96, 173, 7
