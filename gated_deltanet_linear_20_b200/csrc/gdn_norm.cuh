@@ -119,10 +119,10 @@ __device__ __forceinline__ void store_vector(T* p, const F<L::P> (&r)[L::G], int
 
 // One input array in the ring: BEFORE bytes a channel of other arrays lie before
 // it in a stage of ALL bytes a channel.
-template <typename L, typename T, int BEFORE, int ALL>
+template <typename L, typename T, int BEFORE, int ALL, int STAGES = stages<L>(ALL)>
 struct Ring {
   using E = Vec<T, L::V>;
-  static constexpr int kStages = stages<L>(ALL);
+  static constexpr int kStages = STAGES;
   __device__ __forceinline__ static E* slot(unsigned char* smem, int stage, int j) {
     const unsigned threads = L::kShort ? L::TH : blockDim.x;
     E* p = reinterpret_cast<E*>(smem + (stage * ALL + BEFORE) * (threads * L::NV * L::V));
@@ -315,14 +315,22 @@ __device__ __forceinline__ void store_partial(float* part, const F<L::P> (&acc)[
 // Calls f.template run<Layout>() with the layout for rows of D channels: vectors
 // of four where D is a multiple of 4 and every array starts on one (`width` 4: 8
 // bytes of bf16, 16 of fp32), pairs where they start on one, else single channels.
-// LONG: vectors of a thread in rows of 257 to 4096 channels.
-template <int LONG, typename F>
+// Pairs and single channels have layouts of 16 channels a thread before those of 32,
+// whose sums leave the registers (gradients of the residual norm, 2000 x 4097 in bf16:
+// 111 us against 552).
+// LONG: vectors of a thread in rows of 257 to 4096 channels.  TRIM: rows of up to
+// 6144 channels in a layout of their own, whose smaller stages leave room in shared
+// memory (the residual norm's gradients, 2730 x 6144 in bf16: 64 us against 78; its
+// forward pass 36 against 31, so without it).
+template <int LONG, bool TRIM, typename F>
 int with_layout(int D, int width, F&& f) {
   if (width == 4 && D % 4 == 0) {
     if (D <= 64) return f.template run<Layout<8, 256, 2, 4>>();
     if (D <= 128) return f.template run<Layout<16, 256, 2, 4>>();
     if (D <= 256) return f.template run<Layout<32, 256, 2, 4>>();
     if (D <= 4096) return f.template run<Layout<0, 1024 / LONG, LONG, 4>>();
+    if constexpr (TRIM)
+      if (D <= 6144) return f.template run<Layout<0, 384, 4, 4>>();
     if (D <= 8192) return f.template run<Layout<0, 512, 4, 4>>();
     return f.template run<Layout<0, 512, 8, 4>>();
   }
@@ -331,6 +339,7 @@ int with_layout(int D, int width, F&& f) {
     if (D <= 64) return f.template run<Layout<16, 256, 2, 2>>();
     if (D <= 256) return f.template run<Layout<32, 256, 4, 2>>();
     if (D <= 4096) return f.template run<Layout<0, 512, 4, 2>>();
+    if (D <= 8192) return f.template run<Layout<0, 512, 8, 2>>();
     return f.template run<Layout<0, 512, 16, 2>>();
   }
   if (width >= 2) {
@@ -338,10 +347,12 @@ int with_layout(int D, int width, F&& f) {
     if (D < 64) return f.template run<Layout<16, 256, 2, 2, true>>();
     if (D < 256) return f.template run<Layout<32, 256, 4, 2, true>>();
     if (D < 4096) return f.template run<Layout<0, 512, 4, 2, true>>();
+    if (D < 8192) return f.template run<Layout<0, 512, 8, 2, true>>();
     return f.template run<Layout<0, 512, 17, 2, true>>();
   }
   if (D <= 256) return f.template run<Layout<32, 256, 8, 1>>();
   if (D <= 4096) return f.template run<Layout<0, 512, 8, 1>>();
+  if (D <= 8192) return f.template run<Layout<0, 512, 16, 1>>();
   return f.template run<Layout<0, 512, 32, 1>>();
 }
 

@@ -252,10 +252,10 @@ int dispatch(const GatedNormArgs& a, int x_dtype, int dtype, int sms, cudaStream
   using B = __nv_bfloat16;
   const int n = width(a, x_dtype, dtype);
   if (x_dtype == GDN_BF16)
-    return dtype == GDN_BF16 ? with_layout<LONG>(a.D, n, Run<B, B>{a, sms, stream})
-                             : with_layout<LONG>(a.D, n, Run<B, float>{a, sms, stream});
-  return dtype == GDN_BF16 ? with_layout<LONG>(a.D, n, Run<float, B>{a, sms, stream})
-                           : with_layout<LONG>(a.D, n, Run<float, float>{a, sms, stream});
+    return dtype == GDN_BF16 ? with_layout<LONG, false>(a.D, n, Run<B, B>{a, sms, stream})
+                             : with_layout<LONG, false>(a.D, n, Run<B, float>{a, sms, stream});
+  return dtype == GDN_BF16 ? with_layout<LONG, false>(a.D, n, Run<float, B>{a, sms, stream})
+                           : with_layout<LONG, false>(a.D, n, Run<float, float>{a, sms, stream});
 }
 
 }  // namespace

@@ -28,7 +28,7 @@ template <typename L, typename T, typename TR>
 __global__ void __launch_bounds__(L::TH) residual_norm_kernel(const ResidualNormArgs a) {
   constexpr int kAll = 2 * sizeof(T) + sizeof(TR), kStages = stages<L>(kAll);
   constexpr int P = L::P, G = L::G, NV = L::NV;
-  using RR = Ring<L, TR, 0, kAll>;
+  using RR = Ring<L, TR, 0, kAll, kStages>;
   using RX = Ring<L, T, sizeof(TR), kAll>;
   using RZ = Ring<L, T, sizeof(TR) + sizeof(T), kAll>;
   extern __shared__ __align__(16) unsigned char smem[];
@@ -121,19 +121,39 @@ __global__ void __launch_bounds__(L::TH) residual_norm_kernel(const ResidualNorm
 }
 
 // A thread with more than 8 channels has no registers for its inputs and weights
-// beside the sums: it takes each vector again from the ring (or from memory) and
-// the weights from the cache for every pass over the row.
+// beside the sums: for every pass over the row it takes each vector again from the
+// ring (or from memory) and the weights from shared memory, as many of the three as
+// fit behind a ring of two stages, the others from the cache.  In fours only: pairs
+// have no ring and took longer with less of the L1 cache.  (2730 x 6144 and 2048 x
+// 8192 in bf16 64 and 87 us against 93 and 92 with all weights from the cache.  Held
+// to 128 registers although 384 threads may have 168: 64 against 70, and 101 with
+// three stages besides.)
+template <typename L>
+constexpr bool keeps() {
+  return L::NV * L::V <= 8;
+}
+template <typename L>
+constexpr int backward_stages(size_t bytes) {
+  return keeps<L>() ? stages<L>(bytes) : std::min(2, stages<L>(bytes));
+}
+template <typename L>
+constexpr int shared_weights(size_t ring) {  // ring: its bytes a channel
+  return keeps<L>() || L::V < 4 ? 0 : std::min<int>(3, (224 * 1024 - ring * L::kMost) / (4 * L::kMost));
+}
 template <typename L, typename T, typename TR>
-__global__ void __launch_bounds__(L::TH) residual_norm_backward_kernel(const ResidualNormArgs a) {
-  constexpr int kT = sizeof(T), kR = sizeof(TR), kAll = 3 * kT + 2 * kR, kStages = stages<L>(kAll);
+__global__ void __launch_bounds__(keeps<L>() ? L::TH : 512)  // 128 registers also for fewer threads
+    residual_norm_backward_kernel(const ResidualNormArgs a) {
+  constexpr int kT = sizeof(T), kR = sizeof(TR), kAll = 3 * kT + 2 * kR;
+  constexpr int kStages = backward_stages<L>(kAll);
   constexpr int P = L::P, G = L::G, NV = L::NV;
-  constexpr bool kKeep = NV * L::V <= 8;
+  constexpr bool kKeep = keeps<L>();
+  constexpr int kShared = shared_weights<L>(kStages * kAll);
   constexpr int KV = kKeep ? NV : 1;  // vectors kept
-  using RR = Ring<L, TR, 0, kAll>;
-  using RG = Ring<L, TR, kR, kAll>;
-  using RD = Ring<L, T, 2 * kR, kAll>;
-  using RX = Ring<L, T, 2 * kR + kT, kAll>;
-  using RZ = Ring<L, T, 2 * kR + 2 * kT, kAll>;
+  using RR = Ring<L, TR, 0, kAll, kStages>;
+  using RG = Ring<L, TR, kR, kAll, kStages>;
+  using RD = Ring<L, T, 2 * kR, kAll, kStages>;
+  using RX = Ring<L, T, 2 * kR + kT, kAll, kStages>;
+  using RZ = Ring<L, T, 2 * kR + 2 * kT, kAll, kStages>;
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ SumBuffer<L, 3> buf3;
   __shared__ SumBuffer<L, 1> buf1;
@@ -168,15 +188,36 @@ __global__ void __launch_bounds__(L::TH) residual_norm_backward_kernel(const Res
   sum_init(buf3);
   sum_init(buf1);
   F<P> w[KV][G], wp[KV][G], sc[KV][G], dw[NV][G], dwp[NV][G], dsc[NV][G];
-  const auto weights = [&](int j) {
-    F<P>(&wj)[G] = w[kKeep ? j : 0];
-    load_weight<L>(wj, a.w, a.offset, j, at);
-    load_weight<L>(wp[kKeep ? j : 0], a.w_post, a.offset, j, at);
-    load_weight<L>(sc[kKeep ? j : 0], a.scale, 0.f, j, at);
+  // Weight n (w, w_post, scale) of vector j: from memory; its place in shared memory,
+  // which only this thread reads; from there, if it is one of those kept there.
+  const auto load_one = [&](F<P>(&to)[G], int n, int j) {
+    load_weight<L>(to, n == 0 ? a.w : n == 1 ? a.w_post : a.scale, n < 2 ? a.offset : 0.f, j, at);
+  };
+  const auto place = [&](int n, int j) {
+    auto* first = reinterpret_cast<Vec<float, L::V>*>(
+        smem + size_t(blockDim.x) * (NV * L::V) * (kStages * kAll + 4 * n));
+    return first + ((threadIdx.x >> 5) * NV + j) * 32 + (threadIdx.x & 31);
+  };
+  const auto weight = [&](F<P>(&to)[G], int n, int j) {
+    if (n < kShared)
+      spread<L, float>(to, *place(n, j));
+    else
+      load_one(to, n, j);
   };
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    if (kKeep) weights(j);
+    if (kKeep) {
+      load_one(w[j], 0, j);
+      load_one(wp[j], 1, j);
+      load_one(sc[j], 2, j);
+    }
+#pragma unroll
+    for (int n = 0; n < kShared; ++n) {
+      F<P> x[G];
+      load_one(x, n, j);
+#pragma unroll
+      for (int e = 0; e < L::V; ++e) place(n, j)->v[e] = x[e / P].v[e % P];
+    }
 #pragma unroll
     for (int i = 0; i < G; ++i) dw[j][i] = dwp[j][i] = dsc[j][i] = all<P>(0.f);
   }
@@ -222,7 +263,7 @@ __global__ void __launch_bounds__(L::TH) residual_norm_backward_kernel(const Res
       const int k = kKeep ? j : 0;
       if (!kKeep) {
         take(j, false);
-        load_weight<L>(w[k], a.w, a.offset, j, at);
+        weight(w[k], 0, j);
       }
 #pragma unroll
       for (int i = 0; i < G; ++i) {
@@ -242,7 +283,9 @@ __global__ void __launch_bounds__(L::TH) residual_norm_backward_kernel(const Res
       const int k = kKeep ? j : 0;
       if (!kKeep) {
         take(j, true);
-        weights(j);
+        weight(w[k], 0, j);
+        weight(wp[k], 1, j);
+        weight(sc[k], 2, j);
       }
 #pragma unroll
       for (int i = 0; i < G; ++i) {
@@ -276,7 +319,7 @@ __global__ void __launch_bounds__(L::TH) residual_norm_backward_kernel(const Res
         const int k = kKeep ? j : 0;
         if (!kKeep) {
           RX::take(x[k], smem, here, px, j, at, on);
-          load_weight<L>(wp[k], a.w_post, a.offset, j, at);
+          weight(wp[k], 1, j);
 #pragma unroll
           for (int i = 0; i < G; ++i) x[k][i] = mul(x[k][i], rp);
         }
@@ -357,7 +400,8 @@ struct Backward {
     const int grid = even_grid<L>(std::min(
         {groups, (long long)norm_max_parts(a.rows, a.D), (long long)per_sm * sms}));
     constexpr int kBytes = 3 * sizeof(T) + 2 * sizeof(TR);
-    constexpr size_t kThread = stages<L>(kBytes) * L::NV * L::V * kBytes;
+    constexpr int kRing = backward_stages<L>(kBytes) * kBytes;
+    constexpr size_t kThread = L::NV * L::V * size_t(kRing + 4 * shared_weights<L>(kRing));
     if (!raise_smem<&residual_norm_backward_kernel<L, T, TR>>(kThread * L::TH))
       return GDN_ERR_LAUNCH;
     residual_norm_backward_kernel<L, T, TR><<<grid, threads, kThread * threads, stream>>>(a);
@@ -380,13 +424,13 @@ int width(const ResidualNormArgs& a, int dtype, int r_dtype) {
   return ok(4) ? 4 : ok(2) ? 2 : 1;
 }
 
-template <template <typename, typename> class Run, int LONG>
+template <template <typename, typename> class Run, int LONG, bool TRIM>
 int dispatch(const ResidualNormArgs& a, int dtype, int r_dtype, int sms, cudaStream_t stream) {
   using B = __nv_bfloat16;
   const int n = width(a, dtype, r_dtype);
-  if (dtype == GDN_F32) return with_layout<LONG>(a.D, n, Run<float, float>{a, sms, stream});
-  return r_dtype == GDN_BF16 ? with_layout<LONG>(a.D, n, Run<B, B>{a, sms, stream})
-                             : with_layout<LONG>(a.D, n, Run<B, float>{a, sms, stream});
+  if (dtype == GDN_F32) return with_layout<LONG, TRIM>(a.D, n, Run<float, float>{a, sms, stream});
+  return r_dtype == GDN_BF16 ? with_layout<LONG, TRIM>(a.D, n, Run<B, B>{a, sms, stream})
+                             : with_layout<LONG, TRIM>(a.D, n, Run<B, float>{a, sms, stream});
 }
 
 }  // namespace
@@ -412,12 +456,12 @@ int launch_reduce_parts(const float* part, int n, int cols, float* const* dst, i
 
 int launch_residual_norm(const ResidualNormArgs& a, int dtype, int r_dtype, int sms,
                          cudaStream_t stream) {
-  return dispatch<Forward, 4>(a, dtype, r_dtype, sms, stream);
+  return dispatch<Forward, 4, false>(a, dtype, r_dtype, sms, stream);
 }
 
 int launch_residual_norm_backward(const ResidualNormArgs& a, int dtype, int r_dtype, int sms,
                                   cudaStream_t stream) {
-  return dispatch<Backward, 2>(a, dtype, r_dtype, sms, stream);
+  return dispatch<Backward, 2, true>(a, dtype, r_dtype, sms, stream);
 }
 
 }  // namespace gdn

@@ -93,6 +93,25 @@ def test_residual_norm_and_gradients(rows, D, dtype, r_dtype, z, post, scale):
         check_residual_gradients(got, b, dtype, r_dtype, one, summed)
 
 
+# rows of more than a CTA's registers hold with their weights, on more rows than CTAs: the
+# ends of each layout, in fours, pairs, odd rows
+LONG = [(5, 4098), (200, 5120), (3, 6144), (160, 6148), (2, 6150), (301, 8190), (5, 8191), (170, 4997),
+        (299, 5121)]
+
+
+@pytest.mark.parametrize("z,post,scale", [(True, True, True), (False, False, True), (False, True, False)])
+@pytest.mark.parametrize("dtype,r_dtype", [(BF, BF), (BF, F32), (F32, F32)], ids=name_of)
+@pytest.mark.parametrize("rows,D", LONG)
+def test_residual_norm_of_long_rows(rows, D, dtype, r_dtype, z, post, scale):
+    test_residual_norm_and_gradients(rows, D, dtype, r_dtype, z, post, scale)
+
+
+@pytest.mark.parametrize("rows,D", LONG)
+def test_gated_norm_of_long_rows(rows, D):
+    test_gated_norm_and_gradients(rows, D, BF, BF, True, "silu")
+    test_gated_norm_and_gradients(rows, D, F32, BF, True, "sigmoid")
+
+
 def test_rows_of_zeros_and_no_rows():
     w = torch.ones(64, device=DEV)
     x = torch.zeros(3, 64, dtype=BF, device=DEV)
@@ -132,6 +151,24 @@ def test_a_nan_stays_in_its_row():
 def test_unaligned_views_take_the_scalar_path():
     d = ref.norm_inputs(20, 128, x_dtype=BF, dtype=BF, seed=5)
     one, summed = steps(d, 20, 128)
+
+    def shifted(t):
+        flat = torch.empty(t.numel() + 1, dtype=t.dtype, device=DEV)
+        flat[1:] = t.reshape(-1).to(DEV)
+        return flat[1:].view(t.shape)
+
+    s = {k: shifted(v) for k, v in d.items()}
+    want = ref.gated_norm(d)
+    ref.assert_norm(gdn.gated_norm(s["x"], s["w"], s["z"]), (want, want.abs()), one, BF, "y")
+    got = gdn.residual_norm_backward(s["dy"], s["dr_out"], s["x"], s["r"], s["w"], z=s["z"],
+                                     w_post=s["w_post"], scale=s["scale"])
+    check_residual_gradients(got, ref.residual_norm_backward(d), BF, BF, one, summed)
+
+
+@pytest.mark.parametrize("D", [4100, 8192])
+def test_unaligned_long_rows(D):
+    d = ref.norm_inputs(170, D, x_dtype=BF, dtype=BF, seed=6)
+    one, summed = steps(d, 170, D)
 
     def shifted(t):
         flat = torch.empty(t.numel() + 1, dtype=t.dtype, device=DEV)
