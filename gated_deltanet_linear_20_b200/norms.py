@@ -14,7 +14,7 @@ from typing import Optional
 import torch
 
 from .gdn import _lib
-from .recurrence import _F32, _begin, _call, _code, _expect, _optional, _out
+from .recurrence import _F32, _begin, _call, _code, _expect, _fits, _optional, _out
 
 _vp, _ci, _cz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
 for _name, _args in (
@@ -54,6 +54,7 @@ def _rows(x: torch.Tensor, shape):
 
 def workspace_bytes(rows: int, D: int, weights: int = 1) -> int:
     """Bytes of workspace of a backward call with that many weight arrays."""
+    _fits("workspace_bytes", rows, D)
     return int(_lib.gdn_norm_workspace_bytes(rows, D, weights))
 
 

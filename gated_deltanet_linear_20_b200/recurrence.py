@@ -56,12 +56,23 @@ def _code(dtype: torch.dtype, name: str) -> int:
     return code
 
 
+_MOST = 2 ** 31 - 1  # of a size: the library's are C ints, and ctypes keeps their low bits
+
+
+def _fits(what: str, *sizes: int) -> None:
+    if max(sizes, default=0) > _MOST:
+        raise ValueError(f"{what}: sizes must be below 2^31, got {max(sizes)}")
+
+
 def _begin(x: torch.Tensor, what: str, layout: str):
     """x's shape, type, type code and device; ``layout``: its dimensions, e.g. "[B,C]"
-    ("": any)."""
+    ("": rows of its last dimension)."""
     if not isinstance(x, torch.Tensor):
         raise TypeError("x must be a torch.Tensor")
     shape, dtype, device = x.shape, x.dtype, x.device
+    count = x.numel()
+    if count > _MOST or count == 0:
+        _fits(what, *(shape if layout else (*shape[-1:], count // max(1, shape[-1]) if shape else 0)))
     if device.type != "cuda":
         raise ValueError(f"{what} runs on CUDA tensors only (no CPU path)")
     if layout and len(shape) != layout.count(",") + 1:
@@ -132,6 +143,7 @@ def _packed(cu_seqlens, status, dev):
     if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
         raise ValueError("cu_seqlens must be [N+1]")
     N = cu_seqlens.numel() - 1
+    _fits("cu_seqlens", N)
     return (N, _expect(cu_seqlens, "cu_seqlens", _I32, (N + 1,), dev),
             _optional(status, "status", _I32, (1,), dev))
 
