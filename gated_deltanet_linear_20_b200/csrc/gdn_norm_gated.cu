@@ -175,15 +175,15 @@ __global__ void __launch_bounds__(L::TH, L::TH == 512 && L::NV * L::V == 8 ? 2 :
     row_sum<L, 2>(s, buf, turn);
     const float r = rsqrtf(fmaf(s[0], inv, a.eps));
     const F<P> rstd = all<P>(r), c = all<P>(-(s[1] * inv * r * r));  // -mean(u xh) rstd
+    if (on) {  // (with eps = 0 the root of a row that is not there is infinite)
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
+      for (int j = 0; j < NV; ++j) {
 #pragma unroll
-      for (int i = 0; i < G; ++i) {
-        dw[j][i] = fma(dy[j][i], mul(x[j][i], rstd), dw[j][i]);
-        x[j][i] = mul(rstd, fma(c, x[j][i], mul(dy[j][i], w[j][i])));
-        if (a.z) z[j][i] = mul(z[j][i], rstd);
-      }
-      if (on) {
+        for (int i = 0; i < G; ++i) {
+          dw[j][i] = fma(dy[j][i], mul(x[j][i], rstd), dw[j][i]);
+          x[j][i] = mul(rstd, fma(c, x[j][i], mul(dy[j][i], w[j][i])));
+          if (a.z) z[j][i] = mul(z[j][i], rstd);
+        }
         store_vector<L, TX>(static_cast<TX*>(a.dx) + o, x[j], j, at);
         if (a.z) store_vector<L, T>(static_cast<T*>(a.dz) + o, z[j], j, at);
       }

@@ -168,59 +168,62 @@ __global__ void __launch_bounds__(keeps<L>() ? L::TH : 512)  // 128 registers al
     const float rx = a.w_post ? rsqrtf(fmaf(s[2], inv, a.eps)) : 1.f;
     const F<P> rr = all<P>(rs), c = all<P>(-(s[1] * inv * rs * rs)), rp = all<P>(rx);
     F<P> sm = all<P>(0.f);
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int k = kKeep ? j : 0;
-      if (!kKeep) {
-        take(j, true);
-        weight(w[k], 0, j);
-        weight(wp[k], 1, j);
-        weight(sc[k], 2, j);
-      }
-#pragma unroll
-      for (int i = 0; i < G; ++i) {
-        q[k][i] = fma(rr, fma(c, r[k][i], mul(dy[k][i], w[k][i])), q[k][i]);
-        dw[j][i] = fma(dy[k][i], mul(r[k][i], rr), dw[j][i]);
-        x[k][i] = mul(x[k][i], rp);  // xh
-        const F<P> u = mul(x[k][i], wp[k][i]);
-        F<P> qa = q[k][i];
-        if (a.z) {
-          F<P> av, da;
-          gate_slope(a.act, z[k][i], &av, &da);
-          qa = mul(qa, av);
-          z[k][i] = mul(mul(mul(q[k][i], sc[k][i]), u), da);  // dz
-        }
-        dsc[j][i] = fma(qa, u, dsc[j][i]);
-        v[j][i] = mul(qa, sc[k][i]);
-        dwp[j][i] = fma(v[j][i], x[k][i], dwp[j][i]);
-        sm = fma(v[j][i], u, sm);
-      }
-      if (on) {
-        store_vector<L, TR>(static_cast<TR*>(a.dr) + o, q[k], j, at);
-        if (a.z) store_vector<L, T>(static_cast<T*>(a.dz) + o, z[k], j, at);
-      }
-    }
-    if (a.w_post) {
-      float m[1] = {total(sm)};
-      row_sum<L, 1>(m, buf1, turn1);
-      const F<P> e = all<P>(-(m[0] * inv));  // -mean(v w_post xh)
+    if (on) {  // (with eps = 0 the roots of a row that is not there are infinite)
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         const int k = kKeep ? j : 0;
         if (!kKeep) {
-          RX::take(x[k], smem, here, px, j, at, on);
+          take(j, true);
+          weight(w[k], 0, j);
           weight(wp[k], 1, j);
-#pragma unroll
-          for (int i = 0; i < G; ++i) x[k][i] = mul(x[k][i], rp);
+          weight(sc[k], 2, j);
         }
 #pragma unroll
-        for (int i = 0; i < G; ++i)
-          v[j][i] = mul(rp, fma(e, x[k][i], mul(v[j][i], wp[k][i])));
+        for (int i = 0; i < G; ++i) {
+          q[k][i] = fma(rr, fma(c, r[k][i], mul(dy[k][i], w[k][i])), q[k][i]);
+          dw[j][i] = fma(dy[k][i], mul(r[k][i], rr), dw[j][i]);
+          x[k][i] = mul(x[k][i], rp);  // xh
+          const F<P> u = mul(x[k][i], wp[k][i]);
+          F<P> qa = q[k][i];
+          if (a.z) {
+            F<P> av, da;
+            gate_slope(a.act, z[k][i], &av, &da);
+            qa = mul(qa, av);
+            z[k][i] = mul(mul(mul(q[k][i], sc[k][i]), u), da);  // dz
+          }
+          dsc[j][i] = fma(qa, u, dsc[j][i]);
+          v[j][i] = mul(qa, sc[k][i]);
+          dwp[j][i] = fma(v[j][i], x[k][i], dwp[j][i]);
+          sm = fma(v[j][i], u, sm);
+        }
+        store_vector<L, TR>(static_cast<TR*>(a.dr) + o, q[k], j, at);
+        if (a.z) store_vector<L, T>(static_cast<T*>(a.dz) + o, z[k], j, at);
       }
     }
+    float mean = 0.f;  // of v w_post xh
+    if (a.w_post) {
+      float m[1] = {total(sm)};
+      row_sum<L, 1>(m, buf1, turn1);
+      mean = m[0] * inv;
+    }
+    if (on) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
-      if (on) store_vector<L, T>(static_cast<T*>(a.dx) + o, v[j], j, at);
+      for (int j = 0; j < NV; ++j) {
+        if (a.w_post) {
+          const int k = kKeep ? j : 0;
+          if (!kKeep) {
+            RX::take(x[k], smem, here, px, j, at, on);
+            weight(wp[k], 1, j);
+#pragma unroll
+            for (int i = 0; i < G; ++i) x[k][i] = mul(x[k][i], rp);
+          }
+#pragma unroll
+          for (int i = 0; i < G; ++i)
+            v[j][i] = mul(rp, fma(all<P>(-mean), x[k][i], mul(v[j][i], wp[k][i])));
+        }
+        store_vector<L, T>(static_cast<T*>(a.dx) + o, v[j], j, at);
+      }
+    }
     if constexpr (kStages > 0) stage = stage == kStages - 1 ? 0 : stage + 1;
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
