@@ -400,6 +400,8 @@ enum gdn_dtype { GDN_F32 = 0, GDN_BF16 = 1 };
  * The recurrence is computed in fp32 and rounded once, in h.  Runs of tokens
  * are walked in parallel and joined exactly up to rounding, as long as the
  * growth exp(sum of g) over 1024 consecutive tokens stays in the fp32 range.
+ * A decay exp(g) below the normal fp32 numbers counts with the bits it has left;
+ * one below the smallest number (g < -103) may count as zero.
  * Results do not depend on timing (bitwise repeatable on the same device).
  * status: optional device int, as for gdn_prefill: a bounded device wait that
  * gives up stores GDN_ERR_DEVICE_TIMEOUT there.
