@@ -52,22 +52,28 @@ constexpr int kMaxCluster = 8;  // CTAs along time
 constexpr uint64_t kWaitLimitNs = 2000000000;  // 2 s: far beyond any legitimate wait
 constexpr int kMaxSorted = 128;  // packed sequences that are started longest first
 
-// The map of a run of tokens for V channels: c -> A c + H.  A stays finite, so
-// that a state of zero stays out of a run whose growth passes the fp32 range.
+// The map of a run of tokens for V channels: c -> A c + H.  Where the run's growth
+// passes the fp32 range A is infinite and so is what comes of a state, unless that is
+// zero, which stays out of it.
 template <int V>
 struct alignas(8 * V) Map {
   F<V> A, H;
 };
 template <int V>
-__device__ __forceinline__ F<V> finite(F<V> a) {
-#pragma unroll
-  for (int e = 0; e < V; ++e) a.v[e] = fminf(a.v[e], 3.402823466e38f);
-  return a;
-}
-
-template <int V>
 __device__ __forceinline__ F<V> apply(const Map<V>& m, F<V> c) {
-  return fma(m.A, c, m.H);
+  F<V> a = m.A;
+#pragma unroll
+  for (int e = 0; e < V; ++e) a.v[e] = c.v[e] == 0.f ? 0.f : a.v[e];
+  return fma(a, c, m.H);
+}
+// The factor of run x before run y; a decay to nothing in one of them outweighs any
+// growth in the other.
+template <int V>
+__device__ __forceinline__ F<V> join(F<V> x, F<V> y) {
+  F<V> a = mul(x, y);
+#pragma unroll
+  for (int e = 0; e < V; ++e) a.v[e] = x.v[e] == 0.f || y.v[e] == 0.f ? 0.f : a.v[e];
+  return a;
 }
 
 // exp(g) of a joined run: over the whole range.
@@ -224,7 +230,7 @@ __device__ __forceinline__ void scan_exchange(Exchange<V, W>& ex, int round, con
       for (int i = 1; i < W; ++i) {
         const Map<V> y = ex.warp[set][i][lane];
         m.H = apply(y, m.H);
-        m.A = finite(mul(m.A, y.A));
+        m.A = join(m.A, y.A);
       }
       for (unsigned r = w; r < n; r += W)
         store_remote(&ex.cta[set][rank][lane], &ex.bar[set], r, m);
@@ -396,7 +402,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W)
       m.A = add(m.A, to_f(g[i]));
       m.H = fma(al[i], m.H, u[i]);
     }
-    m.A = finite(decay(m.A));
+    m.A = decay(m.A);
     scan_exchange(ex, round, m, carry, h, w, lane, rank, n, &late);
     if (have > 0 && on && a.carries && now % kCarryTokens == 0)
       store<float, V>(a.carries + size_t(s.carry_row + now / kCarryTokens) * a.C + c0, h.v);
@@ -526,7 +532,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W)
     }
 #pragma unroll
     for (int i = S - 1; i >= 0; --i) m.H = mul(al[i], add(to_f(d[i]), m.H));
-    mf.A = m.A = finite(decay(m.A));
+    mf.A = m.A = decay(m.A);
     if (M > 1) fwd[set][sw][lane] = mf;
     scan_exchange(ex, round, m, carry, mu, w, lane, rank, n, &late);
     if (M > 1) {

@@ -399,7 +399,9 @@ enum gdn_dtype { GDN_F32 = 0, GDN_BF16 = 1 };
  *                ceil(T / 16) - 1
  * The recurrence is computed in fp32 and rounded once, in h.  Runs of tokens
  * are walked in parallel and joined exactly up to rounding, as long as the
- * growth exp(sum of g) over 1024 consecutive tokens stays in the fp32 range.
+ * growth exp(sum of g) over any run of up to 128 tokens stays in the fp32 range;
+ * past it a state that is not zero becomes infinite or NaN.  An infinite state
+ * may become NaN.
  * A decay exp(g) below the normal fp32 numbers counts with the bits it has left;
  * one below the smallest number (g < -103) may count as zero.
  * Results do not depend on timing (bitwise repeatable on the same device).
