@@ -177,6 +177,17 @@ int gdn_scan_varlen_backward(const void* x, const float* g, const void* beta, co
                              float* dh0, float* carries, int carries_valid, const int* cu_seqlens,
                              int N, int total_T, int C, int dtype, int* status, void* stream) {
   if (N > 0 && C > 0 && total_T >= 0 && !cu_seqlens) return GDN_ERR_NULL;
+  bool none;
+  const int rc = scan_sizes(N, total_T, C, dtype, &none);
+  if (rc == GDN_OK && N == 0) {  // tokens of no sequence: gradients of zero
+    const size_t act = size_t(total_T) * C, e = elem_size(dtype);
+    const Span grads[] = {{dx, act * e}, {dg, act * 4}, {dbeta, act * e}};
+    for (const Span& d : grads)
+      if (d.p && d.bytes && cudaMemsetAsync(const_cast<void*>(d.p), 0, d.bytes,
+                                            static_cast<cudaStream_t>(stream)) != cudaSuccess)
+        return GDN_ERR_LAUNCH;
+    return GDN_OK;
+  }
   return scan_backward_impl(
       {{x, g, beta, h0, nullptr, nullptr, carries, cu_seqlens, N, total_T, C, 0, status}, dh, dh_T,
        dx, dg, dbeta, dh0},

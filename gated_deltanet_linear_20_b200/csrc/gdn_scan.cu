@@ -428,6 +428,27 @@ __global__ void __launch_bounds__(32 * W, 16 / W)
   exchange_end(n, late, a.status, &ex.full[w], issued);
 }
 
+// Gradients of packed tokens that are before the first sequence or behind the last are
+// zero: the CTAs of a channel block (group `r` of N, CTA `rank` of n in it) share them.
+// Ends of invalid sequences leave everything as it was.
+template <typename T, int V, int W>
+__device__ __forceinline__ void zero_outside(const ScanBackwardArgs& a, int r, unsigned rank,
+                                             unsigned n, int c0) {
+  const ScanArgs& f = a.f;
+  const int* cu = f.cu_seqlens;
+  const int first = cu[0], last = cu[f.N];
+  const int head = first >= 0 && first <= cu[1] && first <= f.T ? first : 0;
+  const int tail = cu[f.N - 1] >= 0 && cu[f.N - 1] <= last && last <= f.T ? last : f.T;
+  const long long rows = (long long)head + (f.T - tail), step = (long long)f.N * n * W;
+  const float zero[V] = {};
+  for (long long k = ((long long)r * n + rank) * W + (threadIdx.x >> 5); k < rows; k += step) {
+    const size_t at = size_t(k < head ? k : tail + (k - head)) * f.C + c0;
+    store<T, V>(static_cast<T*>(a.dx) + at, zero);
+    store<float, V>(a.dg + at, zero);
+    if (a.dbeta) store<T, V>(static_cast<T*>(a.dbeta) + at, zero);
+  }
+}
+
 // Backward: the same walk from the sequence's end.  What passes a token
 // boundary is mu_t = alpha_t lam_t.  h_{t-1} is rebuilt in 32 bits from the
 // states that the forward pass kept every 16 tokens: reading them costs 4/16
@@ -450,6 +471,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W)
   int c0 = (id % f.cblocks) * 32 * V + lane * V;
   const bool on = c0 < f.C;
   if (!on) c0 = f.C - V;
+  if (f.cu_seqlens && on) zero_outside<T, V, W>(a, id / f.cblocks, rank, n, c0);
   Seq s;
   if (!sequence(f, seq, &s)) {
     if (f.status && threadIdx.x == 0 && rank == 0) *f.status = GDN_ERR_SHAPE;

@@ -154,7 +154,8 @@ def scan_varlen(x: torch.Tensor, g: torch.Tensor, cu_seqlens: torch.Tensor,
                 save_carries: bool = False, status: Optional[torch.Tensor] = None):
     """``scan`` of N packed sequences: x, g, beta [total_T,C], cu_seqlens int32
     [N+1] on the device, h0 [N,C]; returns (h [total_T,C], h_T [N,C] fp32), and
-    with ``save_carries`` the kept states ([total_T // 16 + N, C] fp32)."""
+    with ``save_carries`` the kept states ([total_T // 16 + N, C] fp32).  Tokens of no
+    sequence are not written in h: give ``h`` if what is there matters."""
     shape, xt, dt, dev = _begin(x, "scan_varlen", "[total_T,C]")
     T, C = shape
     N, pcu, pst = _packed(cu_seqlens, status, dev)
@@ -232,8 +233,9 @@ def scan_varlen_backward(dh: torch.Tensor, x: torch.Tensor, g: torch.Tensor,
                          h0: Optional[torch.Tensor] = None, dh_T: Optional[torch.Tensor] = None, *,
                          carries: Optional[torch.Tensor] = None,
                          status: Optional[torch.Tensor] = None):
-    """Gradients of ``scan_varlen``'s inputs, as ``scan_backward``.  Gradients of
-    tokens behind the last sequence are not written."""
+    """Gradients of ``scan_varlen``'s inputs, as ``scan_backward``.  Those of tokens
+    before the first sequence and behind the last are zero; those of a sequence with
+    invalid offsets (``status`` reports it) are not written."""
     begun = _begin(x, "scan_varlen_backward", "[total_T,C]")
     T = begun[0][0]
     N, pcu, pst = _packed(cu_seqlens, status, begun[3])

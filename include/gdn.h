@@ -459,8 +459,9 @@ int gdn_scan_backward(const void* x, const float* g, const void* beta, const flo
                       float* dh0, float* carries, int carries_valid, int B, int T, int C,
                       int dtype, int* status, void* stream);
 
-/* gdn_scan_backward of packed sequences (gdn_scan_varlen).  An invalid
- * sequence's gradients are not written. */
+/* gdn_scan_backward of packed sequences (gdn_scan_varlen).  Gradients of tokens
+ * before the first sequence and behind the last are zero (all, without any
+ * sequence); an invalid sequence's are not written. */
 int gdn_scan_varlen_backward(const void* x, const float* g, const void* beta, const float* h0,
                              const void* dh, const float* dh_T, void* dx, float* dg, void* dbeta,
                              float* dh0, float* carries, int carries_valid, const int* cu_seqlens,
