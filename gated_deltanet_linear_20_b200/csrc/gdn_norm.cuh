@@ -252,34 +252,45 @@ __device__ __forceinline__ void row_sum(float (&v)[K], SumBuffer<L, K>& buf, int
   }
 }
 
-// 1 / (1 + exp(-z)) from the approximate power and reciprocal: a few units in
-// the last place of fp32; an overflowing exponential gives 0.
-__device__ __forceinline__ float sigmoid(float z) {
-  float e, p;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.4426950408889634f));
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(p) : "f"(1.f + e));
-  return p;
+// exp(z) and 1 / z by the approximate instructions: two units in the last place and |z|
+// half steps for the product in the exponent; one unit.  Results below the normal
+// numbers are zero, so that a gate below -87.3 is (its value is less than 1e-36; with
+// such results kept 524288 x 128 took 74 us against 69, its gradient 122 against 117).
+__device__ __forceinline__ float power(float z) {
+  float e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * 1.4426950408889634f));
+  return e;
 }
-// The gate's value and slope: p z and p (1 + z (1 - p)), or p and p (1 - p).
+__device__ __forceinline__ float inverse(float z) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(z));
+  return r;
+}
+// The gate's value, with p = 1 / (1 + exp(-z)): p z or p.  An overflowing exponential
+// gives 0.
 template <int P>
 __device__ __forceinline__ F<P> gate(int act, F<P> z) {
   F<P> p;
 #pragma unroll
   for (int e = 0; e < P; ++e) {
-    p.v[e] = sigmoid(z.v[e]);
+    p.v[e] = inverse(1.f + power(-z.v[e]));
     z.v[e] = act == GDN_GATE_SILU ? z.v[e] : 1.f;
   }
   return mul(z, p);
 }
+// Its value and slope, with q = 1 - p = 1 / (1 + exp(z)): p (1 + z q), or p q.  With e =
+// exp(-|z|) the larger of p and q is 1 / (1 + e), the smaller e times that: as a
+// difference q would lose its bits where p is close to one.
 template <int P>
 __device__ __forceinline__ void gate_slope(int act, F<P> z, F<P>* a, F<P>* da) {
-  F<P> p;
+  F<P> p, q;
 #pragma unroll
   for (int e = 0; e < P; ++e) {
-    p.v[e] = sigmoid(z.v[e]);
+    const float x = power(-fabsf(z.v[e])), r = inverse(1.f + x), s = x * r;
+    p.v[e] = z.v[e] < 0.f ? s : r;
+    q.v[e] = z.v[e] < 0.f ? r : s;
     z.v[e] = act == GDN_GATE_SILU ? z.v[e] : 1.f;
   }
-  const F<P> q = fma(p, all<P>(-1.f), all<P>(1.f));
   *a = mul(z, p);
   *da = mul(p, fma(z, q, all<P>(act == GDN_GATE_SILU ? 1.f : 0.f)));
 }

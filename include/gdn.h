@@ -472,6 +472,8 @@ int gdn_scan_varlen_backward(const void* x, const float* g, const void* beta, co
  *   eps           : added to the mean square, finite, >= 0
  *   weight_offset : added to every norm weight (1 for weights kept around zero)
  *   gate          : GDN_GATE_SILU a(z) = z / (1 + exp(-z)), or GDN_GATE_SIGMOID
+ *                   a(z) = 1 / (1 + exp(-z)); where that quotient is below the
+ *                   normal fp32 numbers (z < -87.3) it counts as zero
  * NULL options mean eps = 1e-6, weight_offset = 0, the SiLU gate; invalid ones
  * are GDN_ERR_UNSUPPORTED.  In all four calls rows have D <= 16384 channels
  * (GDN_ERR_SHAPE above), weights and their gradients are fp32 [D], squares and
