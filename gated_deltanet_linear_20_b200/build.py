@@ -21,7 +21,8 @@ CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libgdn_b200.so")
 
 ARCH_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a"]
-NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "--threads", "8", "-Xcompiler", "-fPIC,-O2", "-shared",
+NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "--threads", "8", "--compress-mode=size",
+              "-Xcompiler", "-fPIC,-O2", "-shared",
               "--expt-relaxed-constexpr", "-cudart", "static",
               "-I" + os.path.join(ROOT, "include"), "-I" + CSRC]
 
