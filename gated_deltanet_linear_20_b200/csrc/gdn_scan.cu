@@ -76,27 +76,24 @@ __device__ __forceinline__ F<V> join(F<V> x, F<V> y) {
   return a;
 }
 
-// exp(g) of a joined run: over the whole range.
+// A token's decay, exp(g) as 2^(g log2 e), the power by the approximate instruction
+// (two units in the last place), below the normal numbers too, as a single token's
+// expf.  (Three instructions more than with ftz, which makes those results zero: 32768 x
+// 4096 forward 224 us against 220, 4096 x 2048 21.8 against 20.0; expf for every token
+// 23.8 there; a branch around slices without such decays 266 by its registers.)
 template <int V>
 __device__ __forceinline__ F<V> decay(F<V> g) {
+  g = mul(g, all<V>(1.4426950408889634f));
+#pragma unroll
+  for (int e = 0; e < V; ++e) asm("ex2.approx.f32 %0, %1;" : "=f"(g.v[e]) : "f"(g.v[e]));
+  return g;
+}
+// A run's, from the sum of its log decays.
+template <int V>
+__device__ __forceinline__ F<V> run_decay(F<V> g) {
 #pragma unroll
   for (int e = 0; e < V; ++e) g.v[e] = expf(g.v[e]);
   return g;
-}
-// The decays of a slice, exp(g) as 2^(g log2 e), the power by the approximate
-// instruction (two units in the last place), below the normal numbers too, as a
-// single token's expf.  (Three instructions more than with ftz, which makes those
-// results zero: 4096 x 2048 forward 21.8 us against 20.0, 32768 x 4096 alike; expf
-// for every token 23.8; expf only in slices that have such a decay 25.6 and 254.7
-// against 214, by its registers.)
-template <int V, int S>
-__device__ __forceinline__ void decays(F<V> (&al)[S], const Vec<float, V> (&g)[S]) {
-#pragma unroll
-  for (int i = 0; i < S; ++i) {
-    al[i] = mul(to_f(g[i]), all<V>(1.4426950408889634f));
-#pragma unroll
-    for (int e = 0; e < V; ++e) asm("ex2.approx.f32 %0, %1;" : "=f"(al[i].v[e]) : "f"(al[i].v[e]));
-  }
 }
 
 __device__ __forceinline__ unsigned cluster_size() {
@@ -395,14 +392,14 @@ __global__ void __launch_bounds__(32 * W, 16 / W)
     if (base + step < s.len) place();  // in flight while this slice is worked on
     F<V> al[S], u[S], h;
     Map<V> m{};
-    decays(al, g);
 #pragma unroll
     for (int i = 0; i < S; ++i) {
+      al[i] = decay(to_f(g[i]));
       u[i] = BETA ? mul(to_f(x[i]), to_f(b[BETA ? i : 0])) : to_f(x[i]);
       m.A = add(m.A, to_f(g[i]));
       m.H = fma(al[i], m.H, u[i]);
     }
-    m.A = decay(m.A);
+    m.A = run_decay(m.A);
     scan_exchange(ex, round, m, carry, h, w, lane, rank, n, &late);
     if (have > 0 && on && a.carries && now % kCarryTokens == 0)
       store<float, V>(a.carries + size_t(s.carry_row + now / kCarryTokens) * a.C + c0, h.v);
@@ -546,15 +543,15 @@ __global__ void __launch_bounds__(32 * W, 16 / W)
     };
     F<V> al[S];
     Map<V> m{}, mf{};
-    decays(al, g);
 #pragma unroll
     for (int i = 0; i < S; ++i) {
+      al[i] = decay(to_f(g[i]));
       m.A = add(m.A, to_f(g[i]));
       if (M > 1) mf.H = fma(al[i], mf.H, input(i));
     }
 #pragma unroll
     for (int i = S - 1; i >= 0; --i) m.H = mul(al[i], add(to_f(d[i]), m.H));
-    mf.A = m.A = decay(m.A);
+    mf.A = m.A = run_decay(m.A);
     if (M > 1) fwd[set][sw][lane] = mf;
     scan_exchange(ex, round, m, carry, mu, w, lane, rank, n, &late);
     if (M > 1) {
