@@ -1,8 +1,8 @@
 // The gradients of the step between two blocks (gdn_norm_residual.cuh).
 //
 // Measured (of the measured 6554 GB/s): 4096 x 4096 with everything on and r in fp32
-// 75 us (75%), 8192 x 4096 in bf16 without a gate 98 us (63%).  They are bound by
-// their instructions (67 a channel; a warp issues in half the cycles) and by
+// 75 us (75%), 8192 x 4096 in bf16 without a gate 103 us (60%).  They are bound by
+// their instructions (70 a channel; a warp issues in half the cycles) and by
 // registers: 24 sums, 24 weights and five inputs of 8 channels a thread leave one CTA
 // of 512 threads an SM.
 #include "gdn_norm_residual.cuh"

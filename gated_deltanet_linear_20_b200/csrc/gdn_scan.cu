@@ -27,12 +27,13 @@
 //
 // States, maps and sums are fp32; bf16 is rounded to once, in a result.
 //
-// Measured (bf16 with beta, of the measured 6554 GB/s): forward 32768 x 4096 213 us
-// (96%), 4 x 4096 x 2048 59 us (89%); backward of the latter 111 us (84%).  The
+// Measured (bf16 with beta, of the measured 6554 GB/s): forward 32768 x 4096 209 to 226
+// us (91 to 98%), 4 x 4096 x 2048 59 us (89%); backward of the latter 111 us (84%).  The
 // way there, on 32768 x 4096 forward: 1282 us with joins of exp(sum) at every step
 // and predicated loads, 344 with small CTAs, one product a join and whole slices,
 // 303 with the next slice prefetched, 283 with maps sent by st.async instead of
-// cluster barriers, 207 to 216 with TMA instead of per-thread copies.
+// cluster barriers, 207 to 216 with TMA instead of per-thread copies, and up to 10 us of
+// that for decays and states at the ends of the fp32 range.
 #include <algorithm>
 #include <initializer_list>
 #include <type_traits>
@@ -606,6 +607,8 @@ __global__ void __launch_bounds__(256) scan_step_kernel(const T* x, const float*
 // resident at 128 registers.  In microseconds, forward / backward, at bf16 with beta:
 //   few     (one 16-token slice, or chains enough to fill the GPU one warp each)
 //           64 x 16 x 4096: 12 / 19 against 24 / 27 on four warps
+//           (equal lengths; a far longer sequence among many is walked by these warps
+//           alone: one of 16384 tokens with 127 of 64, 2048 channels, 885 / 1167)
 //   packed  sequences end at different times, so more CTAs are started than are
 //           resident.  8 sequences, 8192 x 2048 (256 chains): 38 / 68 on clusters of
 //           4, 45 / 96 on 2, 45 / 70 on 8; 64, 32768 x 512 (512 chains): 46 / 71, 45
